@@ -14,6 +14,7 @@
 
 #include "../../include/kda.h"
 #include "kda_launch.hpp"
+#include "kda_paged.hpp"
 
 #define KDA_API extern "C" __attribute__((visibility("default")))
 
@@ -33,6 +34,22 @@ kda_status ok() {
   g_err[0] = '\0';
   return KDA_OK;
 }
+
+}  // namespace
+
+// The error channel of the other C-ABI files.
+namespace kda {
+int set_error(int status, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return status;
+}
+int set_ok() { return ok(); }
+}  // namespace kda
+
+namespace {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -1,0 +1,392 @@
+"""The paged attention operators on the GPU against plain 64-bit references
+(tests/paged_ref.py, which also derives the tolerances)."""
+import numpy as np
+import pytest
+import torch
+
+import paged_ref as R
+from gated_delta_rule_65_amd import binding as B
+from gated_delta_rule_65_amd import inputs, paged
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, HF, FP = torch.bfloat16, torch.float16, torch.float32
+
+
+def attend(c, page, window=0, sinks=0, scale=None, **kw):
+    """The operator on the case's tensors, every output pre-filled."""
+    print(f"attend q={tuple(c.q.shape)} cache={tuple(c.k_cache.shape)} {c.q.dtype} "
+          f"window={window} sinks={sinks} {kw}", flush=True)
+    out = torch.full(c.q.shape, 7.0, dtype=c.q.dtype, device=DEV)
+    lse = torch.full(c.q.shape[:2], 7.0, dtype=FP, device=DEV)
+    paged.paged_attention(c.q.to(DEV), c.k_cache.to(DEV), c.v_cache.to(DEV), c.table.to(DEV),
+                          c.cu.to(DEV), c.seq.to(DEV), scale=scale, window=window, sinks=sinks,
+                          output=out, lse=lse, **kw)
+    torch.cuda.synchronize()
+    return out.cpu(), lse.cpu()
+
+
+def check(c, page, got, window=0, sinks=0, scale=None):
+    out, lse = got
+    scale = c.q.shape[-1] ** -0.5 if scale is None else scale
+    ref, rl, tol, tl = R.attention(c, page, scale, window, sinks)
+    T = int(c.cu[-1])
+    o, l = out.double().numpy()[:T], lse.double().numpy()[:T]
+    ref, rl, tol, tl = ref[:T], rl[:T], tol[:T], tl[:T]
+    empty = np.isneginf(rl)
+    assert np.array_equal(np.isneginf(l), empty)
+    assert np.all(o[empty] == 0)
+    worst = np.abs(o - ref) / np.maximum(tol, 1e-300)
+    worst[empty] = 0
+    worst_l = np.where(empty, 0, np.abs(np.where(empty, 0, l) - np.where(empty, 0, rl)) / np.maximum(tl, 1e-300))
+    print(f"  worst share of the tolerance: out {worst.max(initial=0):.3f} lse {worst_l.max(initial=0):.3f}",
+          flush=True)
+    assert worst.max(initial=0) <= 1 and worst_l.max(initial=0) <= 1
+    assert torch.all(out[T:] == 7) and torch.all(lse[T:] == 7)
+
+
+# context, new, hq, hkv, dim, page, dtype, window, sinks
+CASES = {
+    "one_token_alone": ([0], [1], 1, 1, 64, 1, BF, 0, 0),
+    "decode_gqa": ([0, 1, 15, 16, 17, 130, 600], [1] * 7, 8, 2, 128, 16, BF, 0, 0),
+    "decode_mha_fp16": ([5, 63, 64, 300], [1] * 4, 4, 4, 64, 32, HF, 0, 0),
+    "decode_mqa_wide_group": ([40, 333], [1, 1], 40, 1, 128, 16, BF, 0, 0),
+    "decode_fp32": ([0, 31, 32, 257], [1] * 4, 6, 2, 128, 16, FP, 0, 0),
+    "decode_fp32_64": ([77, 0], [1, 1], 5, 1, 64, 20, FP, 0, 0),
+    "draft_tokens": ([10, 0, 255], [4, 3, 5], 8, 2, 128, 16, BF, 0, 0),
+    "odd_page": ([100, 47, 48, 49], [1, 2, 1, 50], 6, 2, 64, 48, HF, 0, 0),
+    "page_of_one": ([70], [3], 2, 1, 64, 1, BF, 0, 0),
+    "page_of_three": ([200, 5], [9, 70], 2, 2, 128, 3, FP, 0, 0),
+    "big_page": ([300, 900], [1, 40], 4, 1, 128, 512, BF, 0, 0),
+    "empty_requests": ([0, 20, 0, 9], [0, 1, 5, 0], 4, 2, 128, 16, BF, 0, 0),
+    "chunk_one_request": ([0], [200], 8, 2, 128, 16, BF, 0, 0),
+    "chunk_group_of_five": ([37], [131], 5, 1, 128, 16, BF, 0, 0),
+    "chunk_long_context": ([1000], [70], 4, 1, 128, 64, HF, 0, 0),
+    "chunks_ragged": ([0, 3, 129, 0, 64], [65, 1, 129, 256, 2], 6, 2, 64, 16, BF, 0, 0),
+    "chunks_fp32": ([3, 100], [65, 17], 6, 2, 128, 16, FP, 0, 0),
+    "window_of_one": ([50, 0], [1, 30], 4, 2, 128, 16, BF, 1, 0),
+    "window_decode_sinks": ([0, 5, 500, 130], [1] * 4, 4, 2, 64, 16, HF, 100, 4),
+    "window_no_sinks": ([300, 0], [80, 200], 4, 1, 128, 16, BF, 64, 0),
+    "window_sinks_chunk": ([300, 0], [80, 333], 4, 1, 128, 16, BF, 33, 7),
+    "window_many_sinks": ([260, 0], [90, 200], 2, 1, 64, 16, BF, 20, 130),
+    "window_past_everything": ([60], [60], 2, 1, 128, 16, BF, 4096, 4),
+    "window_fp32": ([210, 1], [33, 70], 2, 1, 128, 16, FP, 50, 3),
+    "sinks_without_window": ([33], [40], 2, 1, 64, 16, BF, 0, 5),
+}
+
+
+@pytest.mark.parametrize("name", list(CASES))
+@pytest.mark.parametrize("splits", [0, 1, 5])
+def test_attention_matches_64_bits(name, splits):
+    ctx, new, hq, hkv, dim, page, dt, window, sinks = CASES[name]
+    c = R.make(ctx, new, hq, hkv, dim, page, dt, seed=len(name), pad_rows=3)
+    hint = max(new) if splits != 5 else None
+    check(c, page, attend(c, page, window, sinks, splits=splits, max_new_len=hint), window, sinks)
+
+
+@pytest.mark.parametrize("dt", [BF, HF, FP])
+@pytest.mark.parametrize("new", [1, 40])
+def test_strides_padded_pages_and_views(dt, new):
+    """q inside a fused projection, K and V as halves of one pool, a table that is a
+    slice of a wider one."""
+    ctx, news, page = [70, 9], [new, new], 16
+    c = R.make(ctx, news, 4, 2, 128, page, dt, seed=5)
+    T = c.q.shape[0]
+    proj = torch.full((T, 12, 128), float("nan"), dtype=dt)
+    proj[:, 4:8] = c.q
+    pool = torch.stack([c.k_cache, c.v_cache], dim=1).to(DEV)
+    wide = torch.full((2, c.table.shape[1] + 5), -1, dtype=torch.int32)
+    wide[:, 2:2 + c.table.shape[1]] = c.table
+    print("strided views", dt, new, flush=True)
+    out, lse = paged.paged_attention(proj.to(DEV)[:, 4:8], pool[:, 0], pool[:, 1],
+                                     wide.to(DEV)[:, 2:2 + c.table.shape[1]], c.cu.to(DEV),
+                                     c.seq.to(DEV), return_lse=True)
+    torch.cuda.synchronize()
+    check(c, page, (out.cpu(), lse.cpu()))
+
+
+@pytest.mark.parametrize("dt", [BF, HF, FP])
+@pytest.mark.parametrize("ctx,new,window,sinks", [
+    (40, 30, 0, 0), (100, 90, 24, 3), (300, 200, 0, 0), (0, 300, 70, 5)])
+def test_infinite_and_nan_values_stay_where_they_are_seen(dt, ctx, new, window, sinks):
+    """A row gets infinities and NaN of the keys it sees, and of no other."""
+    page = 16
+    c = R.make([ctx], [new], 4, 2, 128, page, dt, seed=9)
+    L = ctx + new
+    for pos, what, side in ((L - 1, float("nan"), "v"), (L - 2, float("inf"), "v"),
+                            (L - 3, float("nan"), "k"), (L // 2, float("inf"), "v")):
+        rows = c.values[0] if side == "v" else c.keys[0]
+        cache = c.v_cache if side == "v" else c.k_cache
+        rows[pos, 0, 5] = what
+        cache[int(c.table[0, pos // page]), 0, pos % page, 5] = what
+    out, _ = attend(c, page, window, sinks)
+    with np.errstate(all="ignore"):
+        ref, _, tol, _ = R.attention(c, page, 128 ** -0.5, window, sinks)
+    o = out.double().numpy()
+    fine = np.isfinite(ref)
+    assert np.array_equal(np.isfinite(o), fine)
+    assert np.array_equal(np.isnan(o), np.isnan(ref))
+    assert np.array_equal(o[np.isinf(ref)], ref[np.isinf(ref)])
+    assert np.all(np.abs(o[fine] - ref[fine]) <= tol[fine])
+
+
+@pytest.mark.parametrize("dt,new", [(BF, 1), (BF, 60), (FP, 20), (HF, 200)])
+def test_missing_pages_hold_no_key(dt, new):
+    """Table entries without a page inside a request, and a row that sees none."""
+    page = 16
+    c = R.make([90, 0], [new, 5], 4, 2, 128, page, dt, seed=4, holes=[(0, 0), (0, 3), (1, 0)])
+    check(c, page, attend(c, page))
+
+
+def test_lengths_below_the_new_tokens_leave_rows_empty():
+    """seq_lens smaller than the request's rows: the first rows lie at negative
+    positions and see nothing."""
+    for dt, new in ((BF, 6), (BF, 100), (FP, 6)):
+        c = R.make([0], [new], 4, 2, 128, 16, dt, seed=2)
+        c.seq[0] = new - 4
+        check(c, 16, attend(c, 16))
+
+
+def test_large_scores_and_growing_maximum():
+    """Scores up to hundreds, growing along the keys, so the running maximum is
+    replaced again and again."""
+    for dt in (BF, HF, FP):
+        c = R.make([400], [70], 2, 1, 64, 16, dt, seed=3)
+        L = 470
+        ramp = torch.linspace(0.1, 8.0, L)[:, None, None]
+        c.keys[0] = (c.keys[0].float() * ramp).to(dt)
+        for j in range(L):
+            c.k_cache[int(c.table[0, j // 16]), :, j % 16] = c.keys[0][j]
+        check(c, 16, attend(c, 16, scale=1.0), scale=1.0)
+        check(c, 16, attend(c, 16, scale=1e-30), scale=1e-30)
+        for scale in (-0.5, 0.0):
+            with pytest.raises(ValueError, match="scale"):
+                attend(c, 16, scale=scale)
+
+
+def test_hint_and_splits_change_sums_only():
+    c = R.make([700, 3, 90], [40, 1, 7], 8, 2, 128, 16, BF, seed=6)
+    for hint in (None, 1, 7, 40, 1000):
+        for splits in (0, 1, 2, 64):
+            check(c, 16, attend(c, 16, max_new_len=hint, splits=splits))
+
+
+def test_equal_calls_give_equal_bits():
+    c = R.make([900, 31], [60, 1], 8, 2, 128, 16, BF, seed=6)
+    a, b = attend(c, 16), attend(c, 16)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# ------------------------------------------------------------- tables, append
+
+TABLES = {
+    "decode": ([0, 15, 16, 17, 100], [1] * 5, 16),
+    "empty_and_zero": ([0, 0, 33, 5], [0, 4, 0, 1], 8),
+    "prefill": ([0, 7, 300], [700, 1, 900], 64),
+    "page_of_one": ([3, 0], [5, 2], 1),
+    "odd_page": ([47, 48, 0, 49], [1, 48, 97, 200], 48),
+    "no_requests": ([], [], 16),
+    "many_requests": ([i % 37 for i in range(2500)], [i % 3 for i in range(2500)], 16),
+    "long_and_many": ([i * 7 % 50 for i in range(1100)], [(i * 31) % 90 for i in range(1100)], 20),
+}
+
+
+def tables_args(ctx, new, page, extra_free=3, cols=None):
+    g = torch.Generator().manual_seed(len(ctx))
+    have = [-(-c // page) for c in ctx]
+    want = [-(-(c + t) // page) for c, t in zip(ctx, new)]
+    num_pages = sum(want) + 5
+    ids = torch.randperm(num_pages, generator=g).to(torch.int32)
+    cols = cols or max(want + [0]) + 2
+    table = torch.full((len(ctx), cols), -5, dtype=torch.int32)
+    at = 0
+    for i, h in enumerate(have):
+        m = min(h, cols)
+        table[i, :m] = ids[at:at + m]
+        at += h
+    free = ids[at:at + sum(want) - sum(have) + extra_free]
+    return free, table, num_pages
+
+
+def run_tables(ctx, new, free, table, page, num_pages, room):
+    t = table.to(DEV)
+    got = paged.page_tables(torch.tensor(ctx, dtype=torch.int32, device=DEV),
+                            torch.tensor(new, dtype=torch.int32, device=DEV), free.to(DEV), t, page,
+                            num_pages, max_tokens=room)
+    torch.cuda.synchronize()
+    return [x.cpu() for x in (*got, t)]
+
+
+@pytest.mark.parametrize("name", list(TABLES))
+def test_tables_match_the_definition(name):
+    ctx, new, page = TABLES[name]
+    free, table, num_pages = tables_args(ctx, new, page)
+    for room in (sum(new), sum(new) + 9, sum(new) + 1500):
+        print("tables", name, room, flush=True)
+        got = run_tables(ctx, new, free, table, page, num_pages, room)
+        ref = R.tables(ctx, new, free, table, page, num_pages, room)
+        for g, r, what in zip(got, ref, ("cu", "seq", "slots", "positions", "taken", "table")):
+            assert torch.equal(g, r), what
+
+
+def test_tables_out_of_pages_bad_entries_and_narrow_tables():
+    ctx, new, page = [10, 40, 0], [30, 30, 50], 16
+    free, table, num_pages = tables_args(ctx, new, page)
+    for f, t, n in ((free[:3], table, num_pages), (free[:0], table, num_pages),
+                    (free, table[:, :3].contiguous(), num_pages), (free, table, 6)):
+        got = run_tables(ctx, new, f, t, page, n, 120)
+        ref = R.tables(ctx, new, f, t, page, n, 120)
+        for g, r, what in zip(got, ref, ("cu", "seq", "slots", "positions", "taken", "table")):
+            assert torch.equal(g, r), what
+
+
+def test_tables_in_a_strided_table_and_given_outputs():
+    ctx, new, page = [10, 40, 0], [30, 30, 50], 16
+    free, table, num_pages = tables_args(ctx, new, page)
+    wide = torch.full((3, table.shape[1] + 7), -9, dtype=torch.int32, device=DEV)
+    view = wide[:, 3:3 + table.shape[1]]
+    view.copy_(table)
+    out = paged.PageTables(*[torch.full((k,), 55, dtype=d, device=DEV) for k, d in (
+        (4, torch.int32), (3, torch.int32), (130, torch.int64), (130, torch.int32), (1, torch.int32))])
+    got = paged.page_tables(torch.tensor(ctx, device=DEV), torch.tensor(new, device=DEV), free.to(DEV),
+                            view, page, num_pages, out=out)
+    assert got is out
+    ref = R.tables(ctx, new, free, table, page, num_pages, 130)
+    for g, r in zip((*out, view), ref):
+        assert torch.equal(g.cpu(), r)
+    assert torch.all(wide[:, :3] == -9) and torch.all(wide[:, 3 + table.shape[1]:] == -9)
+
+
+@pytest.mark.parametrize("dt", [BF, HF, FP])
+@pytest.mark.parametrize("T,hkv,dim,page", [(1, 1, 64, 1), (77, 3, 128, 20), (300, 8, 64, 16), (0, 2, 128, 16)])
+def test_append_copies_rows_to_their_slots(dt, T, hkv, dim, page):
+    g = torch.Generator().manual_seed(T)
+    pages = -(-T // page) + 2
+    proj = torch.randn(T, 2, hkv, dim, generator=g).to(dt)
+    slots = torch.randperm(pages * page, generator=g)[:T]
+    if T > 3:
+        slots[1], slots[3] = -1, pages * page       # padding, and past the cache
+    pool = torch.randn(pages, 2, hkv, page, dim, generator=g).to(dt)
+    want = pool.clone()
+    for t in range(T):
+        s = int(slots[t])
+        if 0 <= s < pages * page:
+            want[s // page, :, :, s % page] = proj[t]
+    d, p = pool.to(DEV), proj.to(DEV)
+    print("append", dt, T, hkv, dim, page, flush=True)
+    paged.kv_append(p[:, 0], p[:, 1], d[:, 0], d[:, 1], slots.to(DEV))
+    torch.cuda.synchronize()
+    assert torch.equal(d.cpu(), want)
+
+
+# ------------------------------------------------------------------- together
+
+def step(ctx, new, k, v, q, kc, vc, table, free, page, window=0, sinks=0, room=None):
+    """One attention layer's step, as a serving loop runs it."""
+    T = q.shape[0]
+    t = paged.page_tables(ctx, new, free, table, page, kc.shape[0], max_tokens=T)
+    paged.kv_append(k, v, kc, vc, t.slot_mapping)
+    return t, paged.paged_attention(q, kc, vc, table, t.cu_seqlens, t.seq_lens, window=window,
+                                    sinks=sinks)
+
+
+def test_steps_of_a_hybrid_batch():
+    """Prefill, then two decode steps, with the tables built on the GPU: each step's
+    attention against the plain form over all rows so far, and the KDA layer of the
+    same batch driven by the same offsets."""
+    hq, hkv, dim, page, dt = 4, 2, 128, 16, BF
+    steps = [[37, 5, 70], [1, 1, 1], [1, 0, 1]]
+    n, num_pages = 3, 12
+    g = torch.Generator().manual_seed(1)
+    table = torch.full((n, 6), -1, dtype=torch.int32, device=DEV)
+    free = torch.randperm(num_pages, generator=g).to(torch.int32).to(DEV)
+    kc = torch.full((num_pages, hkv, page, dim), float("nan"), dtype=dt, device=DEV)
+    vc = kc.clone()
+    ctx = torch.zeros(n, dtype=torch.int32, device=DEV)
+    keys = [torch.zeros(0, hkv, dim, dtype=dt) for _ in range(n)]
+    values = [k.clone() for k in keys]
+    for s, new in enumerate(steps):
+        T = sum(new) + 2                                     # a padded batch
+        q, k, v = (torch.randn(T, h, dim, generator=g).to(dt) for h in (hq, hkv, hkv))
+        print("hybrid step", s, flush=True)
+        t, out = step(ctx, torch.tensor(new, dtype=torch.int32, device=DEV), k.to(DEV), v.to(DEV),
+                      q.to(DEV), kc, vc, table, free, page)
+        torch.cuda.synchronize()
+        at = 0
+        for i, m in enumerate(new):
+            keys[i] = torch.cat([keys[i], k[at:at + m]])
+            values[i] = torch.cat([values[i], v[at:at + m]])
+            at += m
+        c = R.Case(q, kc.cpu(), vc.cpu(), table.cpu(), t.cu_seqlens.cpu(), t.seq_lens.cpu(), keys, values)
+        ref, _, tol, _ = R.attention(c, page, dim ** -0.5)
+        assert np.all(np.abs(out.double().cpu().numpy() - ref)[:at] <= tol[:at])
+        free = free[int(t.pages_taken):].contiguous()
+        ctx = t.seq_lens
+        if s == 0:
+            b = inputs.make_chunk(new, 2, 2, dtype=dt, seed=3)
+            args = [x.to(DEV) for x in (b.q, b.k, b.v, b.g, b.beta)]
+            assert torch.equal(B.chunk_kda(*args, cu_seqlens=t.cu_seqlens),
+                               B.chunk_kda(*args, cu_seqlens=b.cu_seqlens.to(DEV)))
+
+
+def test_another_stream_and_repeated_calls():
+    c = R.make([300, 0], [1, 90], 4, 2, 128, 16, BF, seed=8)
+    args = [x.to(DEV) for x in (c.q, c.k_cache, c.v_cache, c.table, c.cu, c.seq)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        outs = [paged.paged_attention(*args, splits=3) for _ in range(3)]
+    s.synchronize()
+    ref = paged.paged_attention(*args, splits=3)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+
+
+def test_captured_step_replays_match_eager():
+    """Tables, append and attention captured once, replayed on new lengths and rows."""
+    from test_graphs_gpu import capture
+    hq, hkv, dim, page, n, num_pages, T = 4, 2, 64, 16, 5, 60, 40
+    g = torch.Generator().manual_seed(2)
+    ids = torch.randperm(num_pages, generator=g).to(torch.int32).to(DEV)
+    kc = torch.randn(num_pages, hkv, page, dim, generator=g).to(BF).to(DEV)
+    vc = torch.randn(num_pages, hkv, page, dim, generator=g).to(BF).to(DEV)
+    table0 = ids[:30].reshape(5, 6).contiguous()
+    table = torch.cat([table0, torch.full((5, 4), -1, dtype=torch.int32, device=DEV)], 1)
+    free = ids[30:].contiguous()
+    ctx = torch.zeros(n, dtype=torch.int32, device=DEV)
+    new = torch.zeros(n, dtype=torch.int32, device=DEV)
+    q = torch.zeros(T, hq, dim, dtype=BF, device=DEV)
+    k, v = torch.zeros(2, T, hkv, dim, dtype=BF, device=DEV)
+    out = torch.zeros_like(q)
+    room = paged.PageTables(*[torch.zeros(m, dtype=d, device=DEV) for m, d in (
+        (n + 1, torch.int32), (n, torch.int32), (T, torch.int64), (T, torch.int32), (1, torch.int32))])
+    ws = torch.empty(paged.paged_attention_workspace_bytes(q, kc, vc, table, splits=4),
+                     dtype=torch.uint8, device=DEV)
+
+    def run(ins, tab, cache, tabs, o):
+        paged.page_tables(ins[0], ins[1], free, tab, page, num_pages, out=tabs)
+        paged.kv_append(ins[3], ins[4], cache[0], cache[1], tabs.slot_mapping)
+        paged.paged_attention(ins[2], cache[0], cache[1], tab, tabs.cu_seqlens, tabs.seq_lens, output=o,
+                              splits=4, workspace=ws)
+
+    ins, kc0, vc0, tab0 = (ctx, new, q, k, v), kc.clone(), vc.clone(), table.clone()
+    graph = capture(lambda: run(ins, table, (kc, vc), room, out))
+    for r in range(4):
+        lens = torch.randint(0, 90, (n,), generator=g)
+        news = torch.randint(0, 8, (n,), generator=g)
+        for dst, src in zip(ins, (lens, news, torch.randn(T, hq, dim, generator=g),
+                                  torch.randn(T, hkv, dim, generator=g), torch.randn(T, hkv, dim, generator=g))):
+            dst.copy_(src.to(DEV))
+        for dst, src in ((kc, kc0), (vc, vc0), (table, tab0)):
+            dst.copy_(src)
+        out.fill_(3)
+        ekv, etab, eout = (kc0.clone(), vc0.clone()), tab0.clone(), torch.full_like(out, 3)
+        etabs = paged.PageTables(*[x.clone() for x in room])
+        print("captured step replay", r, flush=True)
+        run(ins, etab, ekv, etabs, eout)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eout) and torch.equal(table, etab)
+        assert torch.equal(kc, ekv[0]) and torch.equal(vc, ekv[1])
+        assert all(torch.equal(a, b) for a, b in zip(room, etabs))
