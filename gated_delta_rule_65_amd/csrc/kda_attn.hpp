@@ -57,11 +57,16 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
+__device__ __forceinline__ u32x4v_t lds_read16(uint32_t at) {
+  return *(__attribute__((address_space(3))) const u32x4v_t*)(uintptr_t)at;
+}
+
 // The four 16-bit values of this lane's column: within 16 lanes, lane i points
 // at 4 elements of row i / 4 (columns 4 (i % 4) ..) and receives column i of the
 // 4 x 16 block.
-__device__ __forceinline__ s16x4_t lds_read_tr(const void* p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
+__device__ __forceinline__ s16x4_t lds_read_tr(uint32_t at) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) s16x4_t*)(uintptr_t)at);
 }
 
 // 16-bit operand types of the matrix instructions.
@@ -77,6 +82,7 @@ template <> struct Half<bf16> {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
   static __device__ __forceinline__ void set(frag& f, int j, float x) { f[j] = (__bf16)x; }
+  static __device__ __forceinline__ float widen(uint32_t bits) { return __uint_as_float(bits << 16); }
 };
 template <> struct Half<_Float16> {
   typedef f16x8_t frag;
@@ -91,6 +97,9 @@ template <> struct Half<_Float16> {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
   static __device__ __forceinline__ void set(frag& f, int j, float x) { f[j] = (_Float16)x; }
+  static __device__ __forceinline__ float widen(uint32_t bits) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+  }
 };
 
 // Whether any of the piece's eight 16-bit values is an infinity or a NaN.

@@ -314,10 +314,10 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
       auto v_frag = [&](int d) {
         // columns 16 d + 4 (l16 % 4) .. of rows 4 gq + l16 / 4, and 16 rows on
         const int r = 4 * gq + (l16 >> 2), piece = 2 * d + ((l16 & 3) >> 1);
-        const char* x = (const char*)(vt + r * P + (piece ^ vswz<E, P>(r))) + 8 * (l16 & 1);
-        const char* y = (const char*)(vt + (r + 16) * P + (piece ^ vswz<E, P>(r + 16))) + 8 * (l16 & 1);
+        // (16 rows on, the swizzle is the same)
+        const uint32_t at = lds_addr(vt + r * P + (piece ^ vswz<E, P>(r))) + 8 * (l16 & 1);
         typedef short s16x8_t __attribute__((ext_vector_type(8)));
-        const s16x4_t u = lds_read_tr(x), w = lds_read_tr(y);
+        const s16x4_t u = lds_read_tr(at), w = lds_read_tr(at + 16 * P * 16);
         const s16x8_t z = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
         return __builtin_bit_cast(u32x4v_t, z);
       };

@@ -1,0 +1,297 @@
+// Paged attention of long chunks of new tokens (bf16, fp16).
+//
+// The same one-pass softmax as the rows kernel, with the work of a matrix product:
+// a workgroup holds 32 rows per wave and all its waves walk the keys together, 64
+// at a time, from K and V tiles in LDS that the next ones replace while they are
+// used.  S^T = K Q^T and O^T = V^T P^T run on 32 x 32 x 16 matrix instructions;
+// lane l holds row l % 32 of its wave, in S^T as in O^T, so a row's maximum and sum
+// take one swap between the wave's halves.
+#include "kda_attn.hpp"
+
+namespace kda {
+namespace {
+
+constexpr int KT = 64;          // keys per tile
+constexpr int MIN_TILES = 8;    // key tiles per split at least
+
+__device__ __forceinline__ int kswz(int r) { return r & 7; }
+// The transposing read takes 32 bytes of rows r .. r + 3 at two neighbouring
+// 32-byte columns per half wave: with this the eight fall into different banks.
+template <int P> __device__ __forceinline__ int vswz(int r) {
+  return P == 16 ? 2 * (2 * (r & 3) + ((r >> 2) & 1)) : 2 * ((r & 2) | ((r >> 2) & 1));
+}
+
+template <typename E, int DIM, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
+  typedef typename Half<E>::frag frag;
+  constexpr int P = DIM / 8;            // 16-byte pieces per row
+  constexpr int NI = P / NW > 0 ? P / NW : 1;  // DMA instructions per wave and tile
+  constexpr int QS = DIM / 16, DV = DIM / 32;
+  static_assert(P % NW == 0, "a tile splits evenly over the waves");
+  __shared__ uint4 smem[2][2][KT * P];
+
+  const int lane = threadIdx.x & 63, wave = wave_of();
+  const int l32 = lane & 31, h = lane >> 5;
+  // later tiles have more keys: they go first
+  const int64_t work = (int64_t)gridDim.x - 1 - blockIdx.x;
+  const int kvh = (int)(work % a.hkv), split = blockIdx.y;
+  const RowTile rt = find_tile<32 * NW>(a, (int)(work / a.hkv), lane);
+  if (rt.first >= rt.rows || rt.rows <= a.rows_limit) return;
+  const int rows = min(32 * NW, rt.rows - rt.first);
+  const int seq = max(a.seq[rt.req], 0);
+  const int pos0 = seq - rt.len;
+  const KeyRange<KT> range(a, pos0 + (int)fdiv(rt.first, a.gdiv),
+                           pos0 + (int)fdiv(rt.first + rows - 1, a.gdiv), seq);
+  int per;
+  const int splits = split_of<MIN_TILES>(range.tiles, a.tile_splits, per);
+  if (split >= splits) return;
+  const int t0 = split * per, t1 = min(range.tiles, t0 + per);
+
+  // this lane's row
+  const int r = 32 * wave + l32;
+  const bool in = r < rows;
+  const int tok = (int)fdiv(rt.first + r, a.gdiv);
+  const int head = kvh * a.group + rt.first + r - tok * a.group;
+  const int qpos = pos0 + tok;
+  // positions of the wave's first and last row
+  const int wa = pos0 + (int)fdiv(rt.first + 32 * wave, a.gdiv);
+  const int wb = pos0 + (int)fdiv(rt.first + min(32 * wave + 31, rows - 1), a.gdiv);
+  const bool busy = 32 * wave < rows;
+  frag q[QS];
+  {
+    const uint4* src = reinterpret_cast<const uint4*>(
+        (const E*)a.q + (in ? (int64_t)(rt.start + tok) * a.q_stride + head * DIM : 0));
+#pragma unroll
+    for (int s = 0; s < QS; ++s)
+      q[s] = __builtin_bit_cast(frag, in ? src[2 * s + h] : make_uint4(0, 0, 0, 0));
+  }
+
+  // LDS byte addresses of the fragments in stage 0: key row l32 of a K tile, and the
+  // rows and columns that this lane points the transposing reads at (both swizzles
+  // depend on the row modulo 8 alone, so the other rows are constants away)
+  uint32_t ka[QS], va[DV];
+#pragma unroll
+  for (int x = 0; x < QS; ++x) ka[x] = lds_addr(&smem[0][0][l32 * P + ((2 * x + h) ^ kswz(l32))]);
+#pragma unroll
+  for (int d = 0; d < DV; ++d) {
+    const int i16 = lane & 15, row = 4 * h + (i16 >> 2);
+    const int piece = 4 * d + 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
+    va[d] = lds_addr(&smem[0][1][row * P + (piece ^ vswz<P>(row))]) + 8 * (i16 & 1);
+  }
+  constexpr int STAGE = 2 * KT * P * 16, ROW = P * 16;  // bytes
+
+  f32x16_t o[DV];
+#pragma unroll
+  for (int d = 0; d < DV; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+  float m = NEG_INF, l = 0.0f;
+  const float c = a.scale * LOG2E;
+
+  PageWindow pages(a, rt.req);
+  const char* const kbase = (const char*)a.kc + (int64_t)kvh * a.page.d * (DIM * 2);
+  const char* const vbase = (const char*)a.vc + (int64_t)kvh * a.page.d * (DIM * 2);
+
+  // Issues the DMA of key tile i; returns which of its keys exist.
+  auto issue = [&](int i, int stage) -> uint64_t {
+    const int base = range.base(i);
+    pages.cover(a, (int)fdiv(base, a.page),
+                (int)fdiv(min(base + KT - 1, (int)a.key_capacity - 1), a.page), lane);
+    const int key = base + lane;
+    const int pg = (int)fdiv(key, a.page);
+    int page = pages.at(pg);
+    if (!range.has(key)) page = -1;
+    const int off = key - pg * (int)a.page.d;
+#pragma unroll
+    for (int x = 0; x < NI; ++x) {
+      const int first = 64 * (wave + NW * x);
+      const int slot = first + lane, row = slot / P, ps = slot % P;
+      const int pr = __builtin_amdgcn_ds_bpermute(4 * row, page);
+      const int orow = __builtin_amdgcn_ds_bpermute(4 * row, off);
+      const char* kp = kbase + (int64_t)pr * a.k_page + orow * (DIM * 2) + 16 * (ps ^ kswz(row));
+      const char* vp = vbase + (int64_t)pr * a.v_page + orow * (DIM * 2) + 16 * (ps ^ vswz<P>(row));
+      if (pr < 0) kp = vp = (const char*)&attn_zero;
+      dma16(kp, lds_addr(&smem[stage][0][first]));
+      dma16(vp, lds_addr(&smem[stage][1][first]));
+    }
+    return __ballot(page >= 0);
+  };
+
+  auto sees = [&](int base, uint64_t valid, int j) {
+    const int key = base + j;
+    return ((valid >> j) & 1) && key <= qpos &&
+           (a.window <= 0 || key > qpos - a.window || key < a.sinks);
+  };
+
+  // One key tile.  EDGE: some of its keys are hidden from some rows, or absent.
+  auto compute = [&](auto edge, int base, int stage, uint64_t valid) {
+    constexpr bool EDGE = decltype(edge)::value;
+    f32x16_t s[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int x = 0; x < 16; ++x) s[k][x] = 0.0f;
+#pragma unroll
+      for (int x = 0; x < QS; ++x) {
+        s[k] = Half<E>::mma32(
+            __builtin_bit_cast(frag, lds_read16(ka[x] + stage * STAGE + 32 * k * ROW)), q[x], s[k]);
+      }
+    }
+    if constexpr (EDGE) {
+      // key j = jc + 4 h of the tile against this row, as constants jc against
+      // distances: visible up to `near`, from `far` on, or below `first`
+      const int near = qpos - base - 4 * h, first = a.sinks - base - 4 * h;
+      const int far = a.window > 0 ? near - a.window : -KT;
+      const uint32_t there[2] = {(uint32_t)valid >> (4 * h), (uint32_t)(valid >> 32) >> (4 * h)};
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const int jc = 32 * k + 8 * (x / 4) + x % 4;
+          const bool see = ((there[k] >> (jc & 31)) & 1) && jc <= near && (jc > far || jc < first);
+          s[k][x] = see ? s[k][x] : NEG_INF;
+        }
+    }
+    float mx = NEG_INF;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) mx = fmaxf(mx, s[k][x]);
+    mx = max_half(mx) * c;  // c > 0
+    if (__any(mx > m + LAG)) {
+      const float nm = fmaxf(m, mx);
+      const float f = nm == NEG_INF ? 1.0f : exp2_fast(m - nm);
+      m = nm;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DV; ++d)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[d][x] *= f;
+    }
+    // a row that has seen no key yet keeps m = -inf: its scores are all -inf too
+    const float mb = (m == NEG_INF ? 0.0f : m) - Half<E>::P_BIAS;
+    // P^T as it lies: chunk kc of 16 keys, slots 0..3 keys 4 h + x, slots 4..7 keys 8 + 4 h + x
+    frag p[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const float e = exp2_fast(fmaf(s[k][x], c, -mb));
+        l += e;
+        Half<E>::set(p[2 * k + x / 8], x % 8, e);
+      }
+    uint32_t bad = 0;
+    const uint4* const vt = smem[stage][1];
+    if constexpr (EDGE) {
+#pragma unroll 2
+      for (int x = 0; x < P; ++x) bad |= nonfinite16<E>(vt[64 * x + lane]);
+    }
+    if (!EDGE || !__any(bad)) {
+#pragma unroll
+      for (int d = 0; d < DV; ++d)
+#pragma unroll
+        for (int kc = 0; kc < 4; ++kc) {
+          const uint32_t at = va[d] + stage * STAGE + 16 * kc * ROW;
+          typedef short s16x8_t __attribute__((ext_vector_type(8)));
+          const s16x4_t u = lds_read_tr(at), w = lds_read_tr(at + 8 * ROW);
+          const s16x8_t z = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
+          o[d] = Half<E>::mma32(__builtin_bit_cast(frag, z), p[kc], o[d]);
+        }
+    } else if constexpr (EDGE) {
+      // infinities or NaN in V that some rows must not see (0 times them is NaN):
+      // key by key on the vector unit, added where visible
+#pragma unroll 1
+      for (int j = 0; j < KT; ++j) {
+        // p of key j lies in slot e of chunk j / 16, in half (j / 4) % 2 of the wave
+        const int e = (j & 3) | ((j >> 1) & 4);
+        uint32_t w = 0;
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          w = 4 * (j >> 4) + (e >> 1) == x ? __builtin_bit_cast(u32x4v_t, p[x / 4])[x % 4] : w;
+        const float pj = Half<E>::widen(__shfl(e & 1 ? w >> 16 : w & 0xffffu, l32 + 32 * ((j >> 2) & 1)));
+        const bool see = sees(base, valid, j);
+#pragma unroll
+        for (int d = 0; d < DV; ++d) {
+          __builtin_amdgcn_sched_barrier(0);  // few registers at a time
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const E* v = reinterpret_cast<const E*>(vt + j * P + ((4 * d + x) ^ vswz<P>(j))) + 4 * h;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) o[d][4 * x + y] += see ? pj * to_f32(v[y]) : 0.0f;
+          }
+        }
+      }
+    }
+  };
+
+  if (t0 < t1) {
+    uint64_t valid = issue(t0, 0);
+    for (int i = t0; i < t1; ++i) {
+      const int stage = (i - t0) & 1;
+      // tile i has landed for every wave, and every wave is done with tile i - 1
+      dma_wait<0>();
+      lds_wait();
+      __builtin_amdgcn_s_barrier();
+      uint64_t next = 0;
+      if (i + 1 < t1) next = issue(i + 1, stage ^ 1);
+      const int base = range.base(i);
+      // tiles that none of the wave's rows sees are skipped
+      if (busy && base <= wb &&
+          !(a.window > 0 && base + KT - 1 <= wa - a.window && base >= a.sinks)) {
+        if (base + KT - 1 > wa || valid != ~0ull ||
+            (a.window > 0 && base <= wb - a.window && base + KT > a.sinks))
+          compute(std::true_type{}, base, stage, valid);
+        else
+          compute(std::false_type{}, base, stage, valid);
+      }
+      valid = next;
+    }
+  }
+
+  if (!in) return;
+  l = sum_half(l);
+  // a row that sees no key has l = 0: zeros, and a log-sum-exp of -inf
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float lse2 = l == 0.0f ? NEG_INF : m - Half<E>::P_BIAS + __log2f(l);
+  const int64_t row = (int64_t)(rt.start + tok) * a.hq + head;
+  if (a.part_n != nullptr && split == 0 && h == 0) a.part_n[row] = splits;
+  if (splits == 1) {
+    if (a.lse != nullptr && h == 0) a.lse[row] = lse2 * LN2;
+  } else if (h == 0) {
+    a.part_lse[(int64_t)split * a.total * a.hq + row] = lse2;
+  }
+#pragma unroll
+  for (int d = 0; d < DV; ++d)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      float y[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) y[z] = l == 0.0f ? 0.0f : o[d][4 * x + z] * inv;
+      const int col = 32 * d + 8 * x + 4 * h;
+      if (splits == 1)
+        store4((E*)a.out + row * DIM + col, y[0], y[1], y[2], y[3]);
+      else
+        store4(a.part_o + ((int64_t)split * a.total * a.hq + row) * DIM + col, y[0], y[1], y[2], y[3]);
+    }
+}
+
+template <typename E, int DIM, int NW> hipError_t tiles_go(const AttnLaunch& L) {
+  const int64_t tiles = (int64_t)L.total * L.group / (32 * NW) + L.n;
+  hipLaunchKernelGGL((tiles_kernel<E, DIM, NW>), dim3((unsigned)(tiles * L.hkv), (unsigned)L.tile_splits),
+                     dim3(64 * NW), 0, (hipStream_t)L.stream, L);
+  return hipGetLastError();
+}
+template <typename E, int DIM> hipError_t tiles_nw(const AttnLaunch& L) {
+  return tiles_go<E, DIM, 8>(L);
+}
+template <typename E> hipError_t tiles_dim(const AttnLaunch& L) {
+  return L.dim == 64 ? tiles_nw<E, 64>(L) : tiles_nw<E, 128>(L);
+}
+
+}  // namespace
+
+hipError_t launch_attn_tiles(const AttnLaunch& L) {
+  return L.dtype == 1 ? tiles_dim<bf16>(L) : tiles_dim<_Float16>(L);
+}
+
+}  // namespace kda

@@ -125,22 +125,28 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
   int64_t keys = L.key_capacity;
   if (L.window > 0 && (int64_t)L.window + L.sinks + most_new < keys)
     keys = (int64_t)L.window + L.sinks + most_new;
-  p.row_blocks = most_new * L.group > 16 ? 2 : 1;
-  p.rows_limit = INT32_MAX;
-  p.tile_waves = 0;
-  p.tile_splits = 1;
+  // Requests of up to 32 rows per kv head, and every fp32 one, are the rows kernel's;
+  // a request with more fills the matrix tiles.
+  const int64_t most_rows = most_new * L.group;
+  const bool tiles = a->dtype != KDA_F32 && most_rows > 32;
+  p.row_blocks = most_rows > 16 ? 2 : 1;
+  p.rows_limit = !tiles ? INT32_MAX : a->n > 1 ? 32 : 0;
+  p.tile_waves = tiles ? 8 : 0;
+  const int64_t rows = a->total_tokens * a->hq;
+  const int64_t cap = rows > 0 ? (int64_t)(MAX_PARTIALS / ((size_t)rows * a->head_dim * 4)) : 1;
+  auto splits_of = [&](int64_t base, int64_t wish, int64_t min_keys) {
+    int64_t want = a->splits > 0 ? a->splits : base > 0 ? ceil_div(wish, base) : 1;
+    if (a->splits == 0 && keys > 2048 && want < 4 && min_keys <= 256) want = 4;
+    if (want > MAX_SPLITS) want = MAX_SPLITS;
+    if (want > ceil_div(keys, min_keys)) want = ceil_div(keys, min_keys);
+    if (want > cap) want = cap;
+    return want > 1 ? (int)want : 1;
+  };
   // Enough workgroups for every compute unit, and pieces of long visits small
   // enough to even out ragged lengths.
-  const int64_t base = (int64_t)a->n * a->hkv;
-  int64_t want = base > 0 ? ceil_div(1024, base) : 1;
-  if (keys > 2048 && want < 4) want = 4;
-  if (a->splits > 0) want = a->splits;
-  const int64_t rows = a->total_tokens * a->hq;
-  if (want > MAX_SPLITS) want = MAX_SPLITS;
-  if (want > ceil_div(keys, 256)) want = ceil_div(keys, 256);
-  if (rows > 0 && want > (int64_t)(MAX_PARTIALS / ((size_t)rows * a->head_dim * 4)))
-    want = (int64_t)(MAX_PARTIALS / ((size_t)rows * a->head_dim * 4));
-  p.rows_splits = want > 1 ? (int)want : 1;
+  p.rows_splits = p.rows_limit > 0 ? splits_of((int64_t)a->n * a->hkv, 1024, 256) : 1;
+  p.tile_splits = tiles ? splits_of(ceil_div(a->total_tokens * L.group, 32 * p.tile_waves) * a->hkv,
+                                    256, 512) : 1;
   const int most = p.rows_splits > p.tile_splits ? p.rows_splits : p.tile_splits;
   p.o_bytes = p.lse_bytes = p.n_bytes = 0;
   if (most > 1) {
@@ -272,7 +278,9 @@ KDA_API kda_status kda_paged_attention(const kda_paged_attention_args* a) {
   L.row_blocks = p.row_blocks; L.rows_limit = p.rows_limit; L.rows_splits = p.rows_splits;
   L.tile_waves = p.tile_waves; L.tile_splits = p.tile_splits;
   L.stream = a->stream;
-  hipError_t e = kda::launch_attn_rows(L);
+  hipError_t e = hipSuccess;
+  if (p.tile_waves > 0) e = kda::launch_attn_tiles(L);
+  if (e == hipSuccess && p.rows_limit > 0) e = kda::launch_attn_rows(L);
   if (e == hipSuccess && need > 0) e = kda::launch_attn_join(L);
   if (e != hipSuccess) FAIL(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
   return (kda_status)kda::set_ok();
