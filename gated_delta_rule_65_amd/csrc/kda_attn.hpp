@@ -73,6 +73,7 @@ __device__ __forceinline__ s16x4_t lds_read_tr(uint32_t at) {
 template <typename E> struct Half;
 template <> struct Half<bf16> {
   typedef bf16x8_t frag;
+  typedef bf16x4_t quad;
   static constexpr uint32_t EXP = 0x7f807f80u, CARRY = 0x00800080u;
   static constexpr float P_BIAS = 0.0f;
   static __device__ __forceinline__ f32x4_t mma16(frag a, frag b, f32x4_t c) {
@@ -81,11 +82,17 @@ template <> struct Half<bf16> {
   static __device__ __forceinline__ f32x16_t mma32(frag a, frag b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
-  static __device__ __forceinline__ void set(frag& f, int j, float x) { f[j] = (__bf16)x; }
+  static __device__ __forceinline__ f32x4_t mma16k16(s16x4_t a, quad b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, __builtin_bit_cast(s16x4_t, b), c, 0, 0, 0);
+  }
+  template <typename V> static __device__ __forceinline__ void set(V& f, int j, float x) {
+    f[j] = (__bf16)x;
+  }
   static __device__ __forceinline__ float widen(uint32_t bits) { return __uint_as_float(bits << 16); }
 };
 template <> struct Half<_Float16> {
   typedef f16x8_t frag;
+  typedef _Float16 quad __attribute__((ext_vector_type(4)));
   static constexpr uint32_t EXP = 0x7c007c00u, CARRY = 0x04000400u;
   // Probabilities are scaled by 2^6 so that small ones stay normal numbers of
   // fp16 (the largest is 2^(6 + LAG), well inside its range).
@@ -96,7 +103,12 @@ template <> struct Half<_Float16> {
   static __device__ __forceinline__ f32x16_t mma32(frag a, frag b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
-  static __device__ __forceinline__ void set(frag& f, int j, float x) { f[j] = (_Float16)x; }
+  static __device__ __forceinline__ f32x4_t mma16k16(s16x4_t a, quad b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(quad, a), b, c, 0, 0, 0);
+  }
+  template <typename V> static __device__ __forceinline__ void set(V& f, int j, float x) {
+    f[j] = (_Float16)x;
+  }
   static __device__ __forceinline__ float widen(uint32_t bits) {
     return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
   }
@@ -141,6 +153,17 @@ __device__ __forceinline__ RowTile find_tile(const AttnLaunch& a, int tile, int 
   return t;
 }
 
+// The whole request as one tile to start from.
+__device__ __forceinline__ RowTile request_tile(const AttnLaunch& a, int req) {
+  RowTile t;
+  t.req = req;
+  t.start = min(max(a.cu[req], 0), a.total);
+  t.len = min(max(a.cu[req + 1], t.start), a.total) - t.start;
+  t.rows = t.len * a.group;
+  t.first = 0;
+  return t;
+}
+
 // The key tiles that a row tile with positions pa .. pb visits: those of the
 // sinks [0, sink_end), then those of [lo, end).
 template <int KT> struct KeyRange {
@@ -161,11 +184,10 @@ template <int KT> struct KeyRange {
   __device__ __forceinline__ bool has(int t) const { return t < end && (t >= lo || t < sink_end); }
 };
 
-// Splits of a visit of `tiles` key tiles: at most `splits`, of at least MIN
+// Splits of a visit of `tiles` key tiles: at most `splits`, of at least `least`
 // tiles each; per = tiles of one split.
-template <int MIN>
-__device__ __forceinline__ int split_of(int tiles, int splits, int& per) {
-  per = max(MIN, (tiles + splits - 1) / splits);
+__device__ __forceinline__ int split_of(int tiles, int splits, int least, int& per) {
+  per = max(least, (tiles + splits - 1) / splits);
   return max(1, (tiles + per - 1) / per);
 }
 
@@ -188,6 +210,18 @@ struct PageWindow {
     return __builtin_amdgcn_ds_bpermute(4 * (page - base), entry);
   }
 };
+
+// Bits 0 .. n (none for n < 0) of a word.
+__device__ __forceinline__ uint32_t bits_to(int n) {
+  return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1u;
+}
+// The keys base .. base + 31 that a row at position pos sees, as bits, of those in
+// `there`.
+__device__ __forceinline__ uint32_t seen(const AttnLaunch& a, int base, int pos, uint32_t there) {
+  uint32_t s = there & bits_to(pos - base);
+  if (a.window > 0) s &= ~bits_to(pos - a.window - base) | bits_to(a.sinks - 1 - base);
+  return s;
+}
 
 __device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 

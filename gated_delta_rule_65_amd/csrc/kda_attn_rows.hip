@@ -3,21 +3,22 @@
 //
 // out = softmax(scale q K^T) V over a request's visible keys, in one pass with
 // the running maximum m and sum l of the softmax (exponents in base 2, the scale
-// folded into them).  A workgroup of four waves holds up to 32 rows of one
-// kv head; each wave walks its own quarter of the keys, so no barrier stands in
-// the loop, and the four (m, l, O) are joined through LDS at the end.
+// folded into them).  A workgroup of four waves holds 16 or 32 rows of one kv
+// head; each wave walks its own quarter of the keys, so no barrier stands in the
+// loop, and the four (m, l, O) are joined through LDS at the end.
 //
 // Bound by HBM: a key's K and V rows (512 bytes for 128 bf16 channels) are read
-// once for all rows of the tile.  Each wave keeps a whole tile of 16 KB in flight
-// by DMA into its own LDS double buffer while it works on the one before.
+// once for all rows of the tile.  Each wave keeps a whole tile of 16 keys in flight
+// by DMA into its own LDS double buffer while it works on the one before; with 64 KB
+// a workgroup, two of them share a compute unit, and one streams while the other
+// starts or joins (256 ragged decode requests: 330 us; with tiles of 32 keys and one
+// workgroup per unit, 440 us).
 #include "kda_attn.hpp"
 
 namespace kda {
-
 namespace {
 
 constexpr int WAVES = 4;
-constexpr int MIN_KEYS = 256;  // keys per split at least: two tiles per wave
 
 // Piece p of row r of a K tile sits in slot p ^ (r & 7) of the row (fragment reads
 // have 8 lanes take one piece each of 8 consecutive rows).
@@ -31,12 +32,10 @@ template <typename E, int P> __device__ __forceinline__ int vswz(int r) {
 
 template <typename E, int DIM, int RB> struct Rows {
   static constexpr bool F32 = sizeof(E) == 4;
-  static constexpr int KT = F32 ? 16 : 32;             // keys per tile
+  static constexpr int KT = 16;                         // keys per tile
   static constexpr int P = DIM * (int)sizeof(E) / 16;  // 16-byte pieces per row
   static constexpr int NI = KT * P / 64;               // DMA instructions per K or V tile
-  static constexpr int KB = KT / 16;
   static constexpr int QS = P / 4;                     // Q pieces per lane and row block
-  static constexpr int MIN_TILES = MIN_KEYS / KT;
   static constexpr int STAGE = 2 * KT * P;             // pieces of a K and a V tile
   static constexpr int OS = DIM + 4;                   // floats per joined row (padded)
   static constexpr int JOIN = WAVES * 16 * RB * OS / 4;
@@ -49,10 +48,11 @@ struct Tile {
   uint32_t valid;
 };
 
-template <typename E, int DIM, int RB>
+template <typename E, int DIM, int RB, bool BY_REQUEST>
 __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
   using R = Rows<E, DIM, RB>;
-  constexpr int KT = R::KT, P = R::P, NI = R::NI, KB = R::KB, QS = R::QS;
+  constexpr uint32_t ALL = 0xffffu;
+  constexpr int KT = R::KT, P = R::P, NI = R::NI, QS = R::QS;
   __shared__ uint4 smem[R::PIECES];
   __shared__ float sm_m[WAVES][16 * RB], sm_l[WAVES][16 * RB];
 
@@ -60,147 +60,130 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
   const int l16 = lane & 15, gq = lane >> 4;
   // heads fastest, so that neighbouring workgroups (and one XCD's) share pages
   const int kvh = blockIdx.x % a.hkv, split = blockIdx.y;
-  const RowTile rt = find_tile<16 * RB>(a, blockIdx.x / a.hkv, lane);
-  if (rt.first >= rt.rows || rt.rows > a.rows_limit) return;
-  const int rows = min(16 * RB, rt.rows - rt.first);
+  const RowTile rt = BY_REQUEST ? request_tile(a, blockIdx.x / a.hkv)
+                                : find_tile<16 * RB>(a, blockIdx.x / a.hkv, lane);
+  if (rt.rows > a.rows_limit) return;
   const int seq = max(a.seq[rt.req], 0);
   const int pos0 = seq - rt.len;
-  const int pa = pos0 + (int)fdiv(rt.first, a.gdiv);
-  const int pb = pos0 + (int)fdiv(rt.first + rows - 1, a.gdiv);
-  const KeyRange<KT> range(a, pa, pb, seq);
-  int per;
-  const int splits = split_of<R::MIN_TILES>(range.tiles, a.rows_splits, per);
-  if (split >= splits) return;
-  const int t0 = split * per, nt = max(0, min(per, range.tiles - t0));
-
-  // this lane's rows (the MFMA columns l16 of each block): their queries, zero
-  // past the last row, and their positions
-  uint4 q[RB][QS];
-  int qpos[RB];
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const int r = 16 * b + l16;
-    const int tok = (int)fdiv(rt.first + r, a.gdiv);
-    const int head = kvh * a.group + rt.first + r - tok * a.group;
-    qpos[b] = pos0 + tok;
-    const bool in = r < rows;
-    const uint4* src = reinterpret_cast<const uint4*>(
-        (const E*)a.q + (in ? (int64_t)(rt.start + tok) * a.q_stride + head * DIM : 0));
-#pragma unroll
-    for (int s = 0; s < QS; ++s) q[b][s] = in ? src[4 * s + gq] : make_uint4(0, 0, 0, 0);
-  }
-
-  f32x4_t o[DIM / 16][RB];
-  float m[RB], l[RB];
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    m[b] = NEG_INF;
-    l[b] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < DIM / 16; ++d) o[d][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  }
   const float c = a.scale * LOG2E;
   constexpr float BIAS = [] {
     if constexpr (R::F32) return 0.0f;
     else return Half<E>::P_BIAS;
   }();
-
-  // contiguous tiles per wave
-  const int share = (nt + WAVES - 1) / WAVES;
-  const int w0 = t0 + min(nt, wave * share), w1 = t0 + min(nt, (wave + 1) * share);
   uint4* const my = smem + wave * 2 * R::STAGE;
   PageWindow pages(a, rt.req);
   const char* const kbase = (const char*)a.kc + (int64_t)kvh * a.page.d * (DIM * sizeof(E));
   const char* const vbase = (const char*)a.vc + (int64_t)kvh * a.page.d * (DIM * sizeof(E));
 
-  auto issue = [&](int i, int stage) {
-    Tile t;
-    t.base = range.base(i);
-    pages.cover(a, (int)fdiv(t.base, a.page),
-                (int)fdiv(min(t.base + KT - 1, (int)a.key_capacity - 1), a.page), lane);
-    // lane l looks key l % KT up
-    const int key = t.base + lane % KT;
-    const int pg = (int)fdiv(key, a.page);
-    int page = pages.at(pg);
-    if (!range.has(key)) page = -1;
-    const int off = key - pg * (int)a.page.d;
-    t.valid = (uint32_t)__ballot(page >= 0);
-    if (KT < 32) t.valid &= (1u << (KT & 31)) - 1;
-    uint4* const kt = my + stage * R::STAGE;
-    uint4* const vt = kt + KT * P;
+  // One tile of rows; by request, the further ones of a request that has more
+  // than its hint said.
+  for (int first = rt.first; first < rt.rows; first += BY_REQUEST ? 16 * RB : rt.rows) {
+    const int rows = min(16 * RB, rt.rows - first);
+    const int pa = pos0 + (int)fdiv(first, a.gdiv);
+    const int pb = pos0 + (int)fdiv(first + rows - 1, a.gdiv);
+    const KeyRange<KT> range(a, pa, pb, seq);
+    int per;
+    const int splits = split_of(range.tiles, a.rows_splits, a.rows_min_keys / KT, per);
+    if (split >= splits) continue;
+    const int t0 = split * per, nt = max(0, min(per, range.tiles - t0));
+
+    // this lane's rows (the MFMA columns l16 of each block): their queries, zero
+    // past the last row, and their positions
+    uint4 q[RB][QS];
+    int qpos[RB];
 #pragma unroll
-    for (int i8 = 0; i8 < NI; ++i8) {
-      const int slot = 64 * i8 + lane, r = slot / P, ps = slot % P;
-      const int pr = __builtin_amdgcn_ds_bpermute(4 * r, page);
-      const int orow = __builtin_amdgcn_ds_bpermute(4 * r, off);
-      const char* kp = kbase + (int64_t)pr * a.k_page + orow * (DIM * (int)sizeof(E)) +
-                       16 * (ps ^ kswz(r));
-      const char* vp = vbase + (int64_t)pr * a.v_page + orow * (DIM * (int)sizeof(E)) +
-                       16 * (ps ^ vswz<E, P>(r));
-      if (pr < 0) kp = vp = (const char*)&attn_zero;
-      dma16(kp, lds_addr(kt + 64 * i8));
-      dma16(vp, lds_addr(vt + 64 * i8));
+    for (int b = 0; b < RB; ++b) {
+      const int r = 16 * b + l16;
+      const int tok = (int)fdiv(first + r, a.gdiv);
+      const int head = kvh * a.group + first + r - tok * a.group;
+      qpos[b] = pos0 + tok;
+      const bool in = r < rows;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          (const E*)a.q + (in ? (int64_t)(rt.start + tok) * a.q_stride + head * DIM : 0));
+#pragma unroll
+      for (int s = 0; s < QS; ++s) q[b][s] = in ? src[4 * s + gq] : make_uint4(0, 0, 0, 0);
     }
-    return t;
-  };
 
-  auto sees = [&](const Tile& t, int j, int b) {
-    const int key = t.base + j;
-    return ((t.valid >> j) & 1) && key <= qpos[b] &&
-           (a.window <= 0 || key > qpos[b] - a.window || key < a.sinks);
-  };
+    f32x4_t o[DIM / 16][RB];
+    float m[RB], l[RB];
 
-  // O += P V for a tile whose V holds an infinity or a NaN that some rows must not
-  // see (0 times it is NaN): key by key on the vector unit, added where visible.
-  auto by_key = [&](const Tile& t, const uint4* vt, const f32x4_t (&s)[KB][RB]) {
-#pragma unroll 1
-    for (int j = 0; j < KT; ++j) {
-      float p[RB];
+    auto issue = [&](int i, int stage) {
+      Tile t;
+      t.base = range.base(i);
+      pages.cover(a, (int)fdiv(t.base, a.page),
+                  (int)fdiv(min(t.base + KT - 1, (int)a.key_capacity - 1), a.page), lane);
+      // lane l looks key l % KT up
+      const int key = t.base + lane % KT;
+      const int pg = (int)fdiv(key, a.page);
+      int page = pages.at(pg);
+      if (!range.has(key)) page = -1;
+      const int off = key - pg * (int)a.page.d;
+      t.valid = (uint32_t)__ballot(page >= 0) & ALL;
+      uint4* const kt = my + stage * R::STAGE;
+      uint4* const vt = kt + KT * P;
 #pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        float x = 0.0f;
-#pragma unroll
-        for (int k = 0; k < KB; ++k)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) x = (j >> 4) == k && (j & 3) == r ? s[k][b][r] : x;
-        p[b] = __shfl(x, l16 + 16 * ((j >> 2) & 3));
+      for (int x = 0; x < NI; ++x) {
+        const int slot = 64 * x + lane, r = slot / P, ps = slot % P;
+        const int pr = __builtin_amdgcn_ds_bpermute(4 * r, page);
+        const int orow = __builtin_amdgcn_ds_bpermute(4 * r, off);
+        const char* kp = kbase + (int64_t)pr * a.k_page + orow * (DIM * (int)sizeof(E)) +
+                         16 * (ps ^ kswz(r));
+        const char* vp = vbase + (int64_t)pr * a.v_page + orow * (DIM * (int)sizeof(E)) +
+                         16 * (ps ^ vswz<E, P>(r));
+        if (pr < 0) kp = vp = (const char*)&attn_zero;
+        dma16(kp, lds_addr(kt + 64 * x));
+        dma16(vp, lds_addr(vt + 64 * x));
       }
-#pragma unroll
-      for (int d = 0; d < DIM / 16; ++d) {
-        float v[4];
-        if constexpr (R::F32) {
-          const f32x4_t x =
-              __builtin_bit_cast(f32x4_t, vt[j * P + ((4 * d + gq) ^ vswz<E, P>(j))]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = x[i];
-        } else {
-          const E* x = reinterpret_cast<const E*>(vt + j * P + ((2 * d + (gq >> 1)) ^ vswz<E, P>(j))) +
-                       4 * (gq & 1);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = to_f32(x[i]);
-        }
+      return t;
+    };
+
+    // O += P V key by key on the vector unit, added where the key is visible: for
+    // tiles whose V holds an infinity or a NaN that some rows must not see (0 times
+    // it is NaN).
+    auto by_key = [&](const Tile& t, const uint4* vt, const f32x4_t (&s)[RB]) {
+#pragma unroll 1
+      for (int j = 0; j < KT; ++j) {
+        float p[RB];
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-          const bool see = sees(t, j, b);
+          float x = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[d][b][i] += see ? p[b] * v[i] : 0.0f;
+          for (int r = 0; r < 4; ++r) x = (j & 3) == r ? s[b][r] : x;
+          p[b] = __shfl(x, l16 + 16 * ((j >> 2) & 3));
+        }
+#pragma unroll
+        for (int d = 0; d < DIM / 16; ++d) {
+          float v[4];
+          if constexpr (R::F32) {
+            const f32x4_t x =
+                __builtin_bit_cast(f32x4_t, vt[j * P + ((4 * d + gq) ^ vswz<E, P>(j))]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = x[i];
+          } else {
+            const E* x = reinterpret_cast<const E*>(vt + j * P + ((2 * d + (gq >> 1)) ^ vswz<E, P>(j))) +
+                         4 * (gq & 1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = to_f32(x[i]);
+          }
+#pragma unroll
+          for (int b = 0; b < RB; ++b) {
+            const bool see = (seen(a, t.base, qpos[b], t.valid) >> j) & 1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[d][b][i] += see ? p[b] * v[i] : 0.0f;
+          }
         }
       }
-    }
-  };
+    };
 
-  auto compute = [&](const Tile& t, int stage) {
-    const uint4* const kt = my + stage * R::STAGE;
-    const uint4* const vt = kt + KT * P;
-    f32x4_t s[KB][RB];
+    auto compute = [&](const Tile& t, int stage, bool careful) {
+      const uint4* const kt = my + stage * R::STAGE;
+      const uint4* const vt = kt + KT * P;
+      f32x4_t s[RB];
 #pragma unroll
-    for (int k = 0; k < KB; ++k) {
-#pragma unroll
-      for (int b = 0; b < RB; ++b) s[k][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int b = 0; b < RB; ++b) s[b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < QS; ++i) {
-        const int r = 16 * k + l16;
-        const uint4 kf = kt[r * P + ((4 * i + gq) ^ kswz(r))];
+        const uint4 kf = kt[l16 * P + ((4 * i + gq) ^ kswz(l16))];
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
           if constexpr (R::F32) {
@@ -208,80 +191,79 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
             const f32x4_t y = __builtin_bit_cast(f32x4_t, q[b][i]);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              s[k][b] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], y[e], s[k][b], 0, 0, 0);
+              s[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], y[e], s[b], 0, 0, 0);
           } else {
             typedef typename Half<E>::frag frag;
-            s[k][b] = Half<E>::mma16(__builtin_bit_cast(frag, kf), __builtin_bit_cast(frag, q[b][i]),
-                                     s[k][b]);
+            s[b] = Half<E>::mma16(__builtin_bit_cast(frag, kf), __builtin_bit_cast(frag, q[b][i]), s[b]);
           }
         }
       }
-    }
-    // keys hidden from some rows, or absent
-    const uint32_t all = KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1;
-    const bool mixed = pa != pb && (t.base + KT - 1 > pa ||
-                                    (a.window > 0 && t.base <= pb - a.window && t.base + KT > a.sinks));
-    if (mixed || t.valid != all) {
+      // keys hidden from some rows, or absent
+      const bool mixed = pa != pb && (t.base + KT - 1 > pa ||
+                                      (a.window > 0 && t.base <= pb - a.window && t.base + KT > a.sinks));
+      if (mixed || t.valid != ALL) {
 #pragma unroll
-      for (int k = 0; k < KB; ++k)
+        for (int b = 0; b < RB; ++b) {
+          const uint32_t see = seen(a, t.base, qpos[b], t.valid) >> (4 * gq);
 #pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            s[k][b][r] = sees(t, 16 * k + 4 * gq + r, b) ? s[k][b][r] : NEG_INF;
-          }
-    }
-    // softmax: the maximum over the tile's keys, the rescale where it grew by
-    // more than LAG, the probabilities
-    float mx[RB];
-    bool grew = false;
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      float x = NEG_INF;
-#pragma unroll
-      for (int k = 0; k < KB; ++k)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x = fmaxf(x, s[k][b][r]);
-      mx[b] = max_quarter(x) * c;  // c > 0
-      grew |= mx[b] > m[b] + LAG;
-    }
-    if (__any(grew)) {
+          for (int r = 0; r < 4; ++r) s[b][r] = see & (1u << r) ? s[b][r] : NEG_INF;
+        }
+      }
+      // softmax: the maximum over the tile's keys, the rescale where it grew by
+      // more than LAG, the probabilities
+      float mx[RB];
+      bool grew = false;
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
-        const float nm = fmaxf(m[b], mx[b]);
-        const float f = nm == NEG_INF ? 1.0f : exp2_fast(m[b] - nm);
-        m[b] = nm;
-        l[b] *= f;
+        float x = NEG_INF;
 #pragma unroll
-        for (int d = 0; d < DIM / 16; ++d)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) o[d][b][r] *= f;
+        for (int r = 0; r < 4; ++r) x = fmaxf(x, s[b][r]);
+        mx[b] = max_quarter(x) * c;  // c > 0
+        grew |= mx[b] > m[b] + LAG;
       }
-    }
+      if (__any(grew)) {
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      // a row that has seen no key yet keeps m = -inf: its scores are all -inf too
-      const float mb = (m[b] == NEG_INF ? 0.0f : m[b]) - BIAS;
+        for (int b = 0; b < RB; ++b) {
+          const float nm = fmaxf(m[b], mx[b]);
+          const float f = nm == NEG_INF ? 1.0f : exp2_fast(m[b] - nm);
+          m[b] = nm;
+          l[b] *= f;
 #pragma unroll
-      for (int k = 0; k < KB; ++k)
+          for (int d = 0; d < DIM / 16; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[d][b][r] *= f;
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        // a row that has seen no key yet keeps m = -inf: its scores are all -inf too
+        const float mb = (m[b] == NEG_INF ? 0.0f : m[b]) - BIAS;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float p = exp2_fast(fmaf(s[k][b][r], c, -mb));
-          s[k][b][r] = p;
+          const float p = exp2_fast(fmaf(s[b][r], c, -mb));
+          s[b][r] = p;
           l[b] += p;
         }
-    }
-    if constexpr (R::F32) {
-      bool bad = false;
-      if (mixed) {
+      }
+      if (careful && mixed) {
+        bool bad = false;
+#pragma unroll 2
+        for (int x = 0; x < NI; ++x) {
+          const uint4 u = vt[64 * x + lane];
+          if constexpr (R::F32) {
+            const f32x4_t y = __builtin_bit_cast(f32x4_t, u);
 #pragma unroll
-        for (int i8 = 0; i8 < NI; ++i8) {
-          const f32x4_t x = __builtin_bit_cast(f32x4_t, vt[64 * i8 + lane]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) bad |= !(fabsf(x[e]) < __builtin_inff());
+            for (int e = 0; e < 4; ++e) bad |= !(fabsf(y[e]) < __builtin_inff());
+          } else {
+            bad |= nonfinite16<E>(u) != 0;
+          }
+        }
+        if (__any(bad)) {
+          by_key(t, vt, s);
+          return;
         }
       }
-      if (!__any(bad)) {
+      if constexpr (R::F32) {
         const float* const vf = reinterpret_cast<const float*>(vt);
 #pragma unroll
         for (int d = 0; d < DIM / 16; ++d)
@@ -291,156 +273,195 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
             const float x = vf[r * DIM + (((col >> 2) ^ vswz<E, P>(r)) << 2) + (col & 3)];
 #pragma unroll
             for (int b = 0; b < RB; ++b)
-              o[d][b] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, s[0][b][e], o[d][b], 0, 0, 0);
+              o[d][b] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, s[b][e], o[d][b], 0, 0, 0);
           }
       } else {
-        by_key(t, vt, s);
+        // P^T as it lies: lane group gq holds keys 4 gq + r
+        typename Half<E>::quad p[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) Half<E>::set(p[b], r, s[b][r]);
+#pragma unroll
+        for (int d = 0; d < DIM / 16; ++d) {
+          // columns 16 d + 4 (l16 % 4) .. of row 4 gq + l16 / 4
+          const int r = 4 * gq + (l16 >> 2), piece = 2 * d + ((l16 & 3) >> 1);
+          const s16x4_t v = lds_read_tr(lds_addr(vt + r * P + (piece ^ vswz<E, P>(r))) + 8 * (l16 & 1));
+#pragma unroll
+          for (int b = 0; b < RB; ++b) o[d][b] = Half<E>::mma16k16(v, p[b], o[d][b]);
+        }
       }
-    } else {
-      typedef typename Half<E>::frag frag;
-      // P^T as it lies: slots 0..3 are keys 4 gq + r, slots 4..7 keys 16 + 4 gq + r
-      frag p[RB];
+    };
+
+    // contiguous tiles per wave
+    const int share = (nt + WAVES - 1) / WAVES;
+    const int w0 = t0 + min(nt, wave * share), w1 = t0 + min(nt, (wave + 1) * share);
+    // The second, careful pass is for waves whose sums met an infinity or a NaN.
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        m[b] = NEG_INF;
+        l[b] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DIM / 16; ++d) o[d][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+      if (w0 < w1) {
+        Tile cur = issue(w0, 0);
+#pragma unroll 1
+        for (int i = w0; i < w1; ++i) {
+          const int stage = (i - w0) & 1;
+          Tile next = cur;
+          if (i + 1 < w1) {
+            lds_wait();  // the reads of the tile that this one replaces
+            next = issue(i + 1, stage ^ 1);
+            dma_wait<2 * NI>();
+          } else {
+            dma_wait<0>();
+          }
+          compute(cur, stage, pass > 0);
+          cur = next;
+        }
+      }
+      if (pa == pb) break;  // every key of a tile is visible to all rows
+      float z = 0.0f;       // becomes NaN if any sum is not finite
 #pragma unroll
       for (int b = 0; b < RB; ++b)
 #pragma unroll
-        for (int k = 0; k < KB; ++k)
+        for (int d = 0; d < DIM / 16; ++d)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) Half<E>::set(p[b], 4 * k + r, s[k][b][r]);
-      uint32_t bad = 0;
-      if (mixed) {
-#pragma unroll
-        for (int i8 = 0; i8 < NI; ++i8) bad |= nonfinite16<E>(vt[64 * i8 + lane]);
-      }
-      auto v_frag = [&](int d) {
-        // columns 16 d + 4 (l16 % 4) .. of rows 4 gq + l16 / 4, and 16 rows on
-        const int r = 4 * gq + (l16 >> 2), piece = 2 * d + ((l16 & 3) >> 1);
-        // (16 rows on, the swizzle is the same)
-        const uint32_t at = lds_addr(vt + r * P + (piece ^ vswz<E, P>(r))) + 8 * (l16 & 1);
-        typedef short s16x8_t __attribute__((ext_vector_type(8)));
-        const s16x4_t u = lds_read_tr(at), w = lds_read_tr(at + 16 * P * 16);
-        const s16x8_t z = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
-        return __builtin_bit_cast(u32x4v_t, z);
-      };
-      if (!__any(bad)) {
-#pragma unroll
-        for (int d = 0; d < DIM / 16; ++d) {
-          const frag v = __builtin_bit_cast(frag, v_frag(d));
-#pragma unroll
-          for (int b = 0; b < RB; ++b) o[d][b] = Half<E>::mma16(v, p[b], o[d][b]);
-        }
-      } else {
-        by_key(t, vt, s);
-      }
+          for (int r = 0; r < 4; ++r) z = fmaf(o[d][b][r], 0.0f, z);
+      if (!__any(z != 0.0f)) break;
+      lds_wait();
     }
-  };
 
-  if (w0 < w1) {
-    Tile cur = issue(w0, 0);
-    for (int i = w0; i < w1; ++i) {
-      const int stage = (i - w0) & 1;
-      Tile next = cur;
-      if (i + 1 < w1) {
-        lds_wait();  // the reads of the tile that this one replaces
-        next = issue(i + 1, stage ^ 1);
-        dma_wait<2 * NI>();
-      } else {
-        dma_wait<0>();
+    // join of the four waves
+#pragma unroll
+    for (int b = 0; b < RB; ++b) l[b] = sum_quarter(l[b]);
+    __syncthreads();
+    float* const so = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      const int r = 16 * b + l16;
+      if (gq == 0) {
+        sm_m[wave][r] = m[b];
+        sm_l[wave][r] = l[b];
       }
-      compute(cur, stage);
-      cur = next;
+#pragma unroll
+      for (int d = 0; d < DIM / 16; ++d)
+        *reinterpret_cast<f32x4_t*>(so + (wave * 16 * RB + r) * R::OS + 16 * d + 4 * gq) = o[d][b];
     }
-  }
-
-  // join of the four waves
+    __syncthreads();
+    constexpr int PER = DIM / 4;  // threads per row
+    for (int x = threadIdx.x; x < rows * PER; x += 64 * WAVES) {
+      const int r = x / PER, d = 4 * (x % PER);
+      float top = sm_m[0][r];
 #pragma unroll
-  for (int b = 0; b < RB; ++b) l[b] = sum_quarter(l[b]);
-  __syncthreads();
-  float* const so = reinterpret_cast<float*>(smem);
+      for (int w = 1; w < WAVES; ++w) top = fmaxf(top, sm_m[w][r]);
+      const float base = top == NEG_INF ? 0.0f : top;
+      float sum = 0.0f;
+      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const int r = 16 * b + l16;
-    if (gq == 0) {
-      sm_m[wave][r] = m[b];
-      sm_l[wave][r] = l[b];
+      for (int w = 0; w < WAVES; ++w) {
+        const float f = exp2_fast(sm_m[w][r] - base);
+        sum = fmaf(f, sm_l[w][r], sum);
+        const f32x4_t y = *reinterpret_cast<const f32x4_t*>(so + (w * 16 * RB + r) * R::OS + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(f, y[i], acc[i]);
+      }
+      // a row that sees no key has sum 0: zeros, and a log-sum-exp of -inf
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = sum == 0.0f ? 0.0f : acc[i] * inv;
+      const float lse2 = sum == 0.0f ? NEG_INF : base - BIAS + __log2f(sum);
+      const int tok = (int)fdiv(first + r, a.gdiv);
+      const int head = kvh * a.group + first + r - tok * a.group;
+      const int64_t row = (int64_t)(rt.start + tok) * a.hq + head;
+      if (a.part_n != nullptr && split == 0 && d == 0) a.part_n[row] = splits;
+      if (splits == 1) {
+        store4((E*)a.out + row * DIM + d, acc[0], acc[1], acc[2], acc[3]);
+        if (a.lse != nullptr && d == 0) a.lse[row] = lse2 * LN2;
+      } else {
+        const int64_t prow = (int64_t)split * a.total * a.hq + row;
+        store4(a.part_o + prow * DIM + d, acc[0], acc[1], acc[2], acc[3]);
+        if (d == 0) a.part_lse[prow] = lse2;
+      }
     }
-#pragma unroll
-    for (int d = 0; d < DIM / 16; ++d)
-      *reinterpret_cast<f32x4_t*>(so + (wave * 16 * RB + r) * R::OS + 16 * d + 4 * gq) = o[d][b];
-  }
-  __syncthreads();
-  constexpr int PER = DIM / 4;  // threads per row
-  for (int x = threadIdx.x; x < rows * PER; x += 64 * WAVES) {
-    const int r = x / PER, d = 4 * (x % PER);
-    float top = sm_m[0][r];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) top = fmaxf(top, sm_m[w][r]);
-    const float base = top == NEG_INF ? 0.0f : top;
-    float sum = 0.0f;
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      const float f = exp2_fast(sm_m[w][r] - base);
-      sum = fmaf(f, sm_l[w][r], sum);
-      const f32x4_t y = *reinterpret_cast<const f32x4_t*>(so + (w * 16 * RB + r) * R::OS + d);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fmaf(f, y[i], acc[i]);
-    }
-    // a row that sees no key has sum 0: zeros, and a log-sum-exp of -inf
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = sum == 0.0f ? 0.0f : acc[i] * inv;
-    const float lse2 = sum == 0.0f ? NEG_INF : base - BIAS + __log2f(sum);
-    const int tok = (int)fdiv(rt.first + r, a.gdiv);
-    const int head = kvh * a.group + rt.first + r - tok * a.group;
-    const int64_t row = (int64_t)(rt.start + tok) * a.hq + head;
-    if (a.part_n != nullptr && split == 0 && d == 0) a.part_n[row] = splits;
-    if (splits == 1) {
-      store4((E*)a.out + row * DIM + d, acc[0], acc[1], acc[2], acc[3]);
-      if (a.lse != nullptr && d == 0) a.lse[row] = lse2 * LN2;
-    } else {
-      const int64_t prow = (int64_t)split * a.total * a.hq + row;
-      store4(a.part_o + prow * DIM + d, acc[0], acc[1], acc[2], acc[3]);
-      if (d == 0) a.part_lse[prow] = lse2;
-    }
+    if (BY_REQUEST) __syncthreads();  // before the next tile's DMA
   }
 }
 
-// out = sum_s 2^(lse_s - top) O_s / sum_s 2^(lse_s - top) over a row's splits.
-// One wave per row; rows that were not split are already in out.
-template <typename E, int DIM>
-__global__ __launch_bounds__(256) void join_kernel(const AttnLaunch a, int splits) {
-  const int lane = threadIdx.x & 63;
+// out = sum_s 2^(lse_s - top) O_s / sum_s 2^(lse_s - top) over the splits of a row,
+// in their order.  W waves share a row's splits (many splits, few rows), or each
+// wave takes `each` consecutive rows of which only some were split.
+template <typename E, int DIM, int W>
+__global__ __launch_bounds__(256) void join_kernel(const AttnLaunch a, int splits, int each) {
+  constexpr int V = DIM / 64;
+  __shared__ float sm[W > 1 ? W : 1][DIM];
+  const int lane = threadIdx.x & 63, wave = wave_of();
   const int64_t rows = (int64_t)a.total * a.hq;
-  const int64_t row = (int64_t)blockIdx.x * 4 + wave_of();
   // only the rows of the batch have partials
   const int64_t first = (int64_t)min(max(a.cu[0], 0), a.total) * a.hq;
   const int64_t last = (int64_t)min(max(a.cu[a.n], 0), a.total) * a.hq;
-  if (row < first || row >= last) return;
-  const int n = min(a.part_n[row], splits);
-  if (n <= 1) return;
-  constexpr int V = DIM / 64;
-  float top = NEG_INF;
-  for (int s = 0; s < n; ++s) top = fmaxf(top, a.part_lse[s * rows + row]);
-  const float base = top == NEG_INF ? 0.0f : top;
-  float sum = 0.0f, acc[V] = {};
-  for (int s = 0; s < n; ++s) {
-    const float f = exp2_fast(a.part_lse[s * rows + row] - base);
-    const float* src = a.part_o + (s * rows + row) * DIM + V * lane;
-    sum += f;
+  const int64_t r0 = W > 1 ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x * 4 + wave) * each;
+  // lane i finds out about row r0 + i
+  int cut = 1;
+  if (lane < each && r0 + lane >= first && r0 + lane < last) cut = a.part_n[r0 + lane];
+  uint64_t todo = __ballot(cut > 1);
+  while (todo != 0) {
+    const int at = __builtin_ctzll(todo);
+    todo &= todo - 1;
+    const int64_t row = r0 + at;
+    const int n = min(__builtin_amdgcn_readlane(cut, at), splits);
+    // lane s weighs split s
+    const float e = lane < n ? a.part_lse[lane * rows + row] : NEG_INF;
+    float top = e;
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = fmaf(f, src[i], acc[i]);
+    for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    const float base = top == NEG_INF ? 0.0f : top;
+    const float f = exp2_fast(e - base);
+    float sum = f;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    const int w = W > 1 ? wave : 0, share = (n + W - 1) / W;
+    float acc[V] = {};
+    const float* src = a.part_o + row * DIM + V * lane;
+#pragma unroll 8
+    for (int s = w * share; s < min(n, (w + 1) * share); ++s) {
+      const float g = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(g, src[s * rows * DIM + i], acc[i]);
+    }
+    if (W > 1) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) sm[wave][V * lane + i] = acc[i];
+      __syncthreads();
+      if (wave != 0) return;
+#pragma unroll
+      for (int x = 1; x < W; ++x)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += sm[x][V * lane + i];
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    E* dst = (E*)a.out + row * DIM + V * lane;
+#pragma unroll
+    for (int i = 0; i < V; ++i) dst[i] = from_f32<E>(acc[i] * inv);
+    if (a.lse != nullptr && lane == 0)
+      a.lse[row] = sum == 0.0f ? NEG_INF : (base + __log2f(sum)) * LN2;
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  E* dst = (E*)a.out + row * DIM + V * lane;
-#pragma unroll
-  for (int i = 0; i < V; ++i) dst[i] = from_f32<E>(acc[i] * inv);
-  if (a.lse != nullptr && lane == 0) a.lse[row] = sum == 0.0f ? NEG_INF : (base + __log2f(sum)) * LN2;
 }
 
 template <typename E, int DIM, int RB> hipError_t rows_go(const AttnLaunch& L) {
-  const int64_t tiles = (int64_t)L.total * L.group / (16 * RB) + L.n;
-  hipLaunchKernelGGL((rows_kernel<E, DIM, RB>), dim3((unsigned)(tiles * L.hkv), (unsigned)L.rows_splits),
-                     dim3(64 * WAVES), 0, (hipStream_t)L.stream, L);
+  if (L.by_request) {
+    hipLaunchKernelGGL((rows_kernel<E, DIM, RB, true>),
+                       dim3((unsigned)(L.n * L.hkv), (unsigned)L.rows_splits), dim3(64 * WAVES), 0,
+                       (hipStream_t)L.stream, L);
+  } else {
+    const int64_t tiles = (int64_t)L.total * L.group / (16 * RB) + L.n;
+    hipLaunchKernelGGL((rows_kernel<E, DIM, RB, false>),
+                       dim3((unsigned)(tiles * L.hkv), (unsigned)L.rows_splits), dim3(64 * WAVES), 0,
+                       (hipStream_t)L.stream, L);
+  }
   return hipGetLastError();
 }
 template <typename E, int DIM> hipError_t rows_rb(const AttnLaunch& L) {
@@ -449,14 +470,24 @@ template <typename E, int DIM> hipError_t rows_rb(const AttnLaunch& L) {
 template <typename E> hipError_t rows_dim(const AttnLaunch& L) {
   return L.dim == 64 ? rows_rb<E, 64>(L) : rows_rb<E, 128>(L);
 }
-template <typename E> hipError_t join_dim(const AttnLaunch& L) {
+
+// Four waves share a row where there are many splits of few rows; with many rows,
+// most of which were not split, a wave looks at 16 of them.
+template <typename E, int DIM> hipError_t join_go(const AttnLaunch& L) {
   const int splits = L.rows_splits > L.tile_splits ? L.rows_splits : L.tile_splits;
-  const unsigned blocks = (unsigned)(((int64_t)L.total * L.hq + 3) / 4);
-  if (L.dim == 64)
-    hipLaunchKernelGGL((join_kernel<E, 64>), dim3(blocks), dim3(256), 0, (hipStream_t)L.stream, L, splits);
-  else
-    hipLaunchKernelGGL((join_kernel<E, 128>), dim3(blocks), dim3(256), 0, (hipStream_t)L.stream, L, splits);
+  const int64_t rows = (int64_t)L.total * L.hq;
+  if (splits > 8 && rows <= 8192) {
+    hipLaunchKernelGGL((join_kernel<E, DIM, 4>), dim3((unsigned)rows), dim3(256), 0,
+                       (hipStream_t)L.stream, L, splits, 1);
+  } else {
+    const int each = rows <= 16384 ? 1 : 16;
+    hipLaunchKernelGGL((join_kernel<E, DIM, 1>), dim3((unsigned)((rows + 4 * each - 1) / (4 * each))),
+                       dim3(256), 0, (hipStream_t)L.stream, L, splits, each);
+  }
   return hipGetLastError();
+}
+template <typename E> hipError_t join_dim(const AttnLaunch& L) {
+  return L.dim == 64 ? join_go<E, 64>(L) : join_go<E, 128>(L);
 }
 
 }  // namespace

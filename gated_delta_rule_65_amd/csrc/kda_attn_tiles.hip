@@ -12,7 +12,6 @@ namespace kda {
 namespace {
 
 constexpr int KT = 64;          // keys per tile
-constexpr int MIN_TILES = 8;    // key tiles per split at least
 
 __device__ __forceinline__ int kswz(int r) { return r & 7; }
 // The transposing read takes 32 bytes of rows r .. r + 3 at two neighbouring
@@ -43,7 +42,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   const KeyRange<KT> range(a, pos0 + (int)fdiv(rt.first, a.gdiv),
                            pos0 + (int)fdiv(rt.first + rows - 1, a.gdiv), seq);
   int per;
-  const int splits = split_of<MIN_TILES>(range.tiles, a.tile_splits, per);
+  const int splits = split_of(range.tiles, a.tile_splits, a.tile_min_keys / KT, per);
   if (split >= splits) return;
   const int t0 = split * per, t1 = min(range.tiles, t0 + per);
 
@@ -81,11 +80,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   constexpr int STAGE = 2 * KT * P * 16, ROW = P * 16;  // bytes
 
   f32x16_t o[DV];
-#pragma unroll
-  for (int d = 0; d < DV; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
-  float m = NEG_INF, l = 0.0f;
+  float m, l;
   const float c = a.scale * LOG2E;
 
   PageWindow pages(a, rt.req);
@@ -117,15 +112,10 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
     return __ballot(page >= 0);
   };
 
-  auto sees = [&](int base, uint64_t valid, int j) {
-    const int key = base + j;
-    return ((valid >> j) & 1) && key <= qpos &&
-           (a.window <= 0 || key > qpos - a.window || key < a.sinks);
-  };
-
   // One key tile.  EDGE: some of its keys are hidden from some rows, or absent.
-  auto compute = [&](auto edge, int base, int stage, uint64_t valid) {
-    constexpr bool EDGE = decltype(edge)::value;
+  // CAREFUL: V may hold infinities or NaN at the hidden ones.
+  auto compute = [&](auto edge, auto careful, int base, int stage, uint64_t valid) {
+    constexpr bool EDGE = decltype(edge)::value, CAREFUL = decltype(careful)::value;
     f32x16_t s[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -138,19 +128,13 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
       }
     }
     if constexpr (EDGE) {
-      // key j = jc + 4 h of the tile against this row, as constants jc against
-      // distances: visible up to `near`, from `far` on, or below `first`
-      const int near = qpos - base - 4 * h, first = a.sinks - base - 4 * h;
-      const int far = a.window > 0 ? near - a.window : -KT;
-      const uint32_t there[2] = {(uint32_t)valid >> (4 * h), (uint32_t)(valid >> 32) >> (4 * h)};
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t see = seen(a, base + 32 * k, qpos, (uint32_t)(valid >> (32 * k))) >> (4 * h);
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const int jc = 32 * k + 8 * (x / 4) + x % 4;
-          const bool see = ((there[k] >> (jc & 31)) & 1) && jc <= near && (jc > far || jc < first);
-          s[k][x] = see ? s[k][x] : NEG_INF;
-        }
+        for (int x = 0; x < 16; ++x)
+          s[k][x] = see & (1u << (8 * (x / 4) + x % 4)) ? s[k][x] : NEG_INF;
+      }
     }
     float mx = NEG_INF;
 #pragma unroll
@@ -180,13 +164,16 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
         l += e;
         Half<E>::set(p[2 * k + x / 8], x % 8, e);
       }
-    uint32_t bad = 0;
     const uint4* const vt = smem[stage][1];
-    if constexpr (EDGE) {
+    bool plain = true;
+    if constexpr (CAREFUL) {
+      __builtin_amdgcn_sched_barrier(0);  // few registers at a time on this path
+      uint32_t bad = 0;
 #pragma unroll 2
       for (int x = 0; x < P; ++x) bad |= nonfinite16<E>(vt[64 * x + lane]);
+      plain = !__any(bad);
     }
-    if (!EDGE || !__any(bad)) {
+    if (!CAREFUL || plain) {
 #pragma unroll
       for (int d = 0; d < DV; ++d)
 #pragma unroll
@@ -197,7 +184,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
           const s16x8_t z = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
           o[d] = Half<E>::mma32(__builtin_bit_cast(frag, z), p[kc], o[d]);
         }
-    } else if constexpr (EDGE) {
+    } else if constexpr (CAREFUL) {
       // infinities or NaN in V that some rows must not see (0 times them is NaN):
       // key by key on the vector unit, added where visible
 #pragma unroll 1
@@ -209,23 +196,38 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
         for (int x = 0; x < 16; ++x)
           w = 4 * (j >> 4) + (e >> 1) == x ? __builtin_bit_cast(u32x4v_t, p[x / 4])[x % 4] : w;
         const float pj = Half<E>::widen(__shfl(e & 1 ? w >> 16 : w & 0xffffu, l32 + 32 * ((j >> 2) & 1)));
-        const bool see = sees(base, valid, j);
+        // all ones where this row sees the key
+        const uint32_t see =
+            0u - ((seen(a, base + (j & 32), qpos, (uint32_t)(valid >> (j & 32))) >> (j & 31)) & 1);
 #pragma unroll
         for (int d = 0; d < DV; ++d) {
           __builtin_amdgcn_sched_barrier(0);  // few registers at a time
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const E* v = reinterpret_cast<const E*>(vt + j * P + ((4 * d + x) ^ vswz<P>(j))) + 4 * h;
+            const uint2 u = *reinterpret_cast<const uint2*>(
+                reinterpret_cast<const char*>(vt + j * P + ((4 * d + x) ^ vswz<P>(j))) + 8 * h);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) o[d][4 * x + y] += see ? pj * to_f32(v[y]) : 0.0f;
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t v = (y < 2 ? u.x : u.y) & see;
+              o[d][4 * x + y] = fmaf(pj, Half<E>::widen(y & 1 ? v >> 16 : v & 0xffffu), o[d][4 * x + y]);
+            }
           }
         }
       }
     }
   };
 
-  if (t0 < t1) {
-    uint64_t valid = issue(t0, 0);
+  auto walk = [&](auto careful) {
+    constexpr bool CAREFUL = decltype(careful)::value;
+    m = NEG_INF;
+    l = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DV; ++d)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o[d][x] = 0.0f;
+    uint64_t valid = 0;
+    if (t0 < t1) valid = issue(t0, 0);
+#pragma unroll 1
     for (int i = t0; i < t1; ++i) {
       const int stage = (i - t0) & 1;
       // tile i has landed for every wave, and every wave is done with tile i - 1
@@ -238,14 +240,25 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
       // tiles that none of the wave's rows sees are skipped
       if (busy && base <= wb &&
           !(a.window > 0 && base + KT - 1 <= wa - a.window && base >= a.sinks)) {
-        if (base + KT - 1 > wa || valid != ~0ull ||
+        if (CAREFUL || base + KT - 1 > wa || valid != ~0ull ||
             (a.window > 0 && base <= wb - a.window && base + KT > a.sinks))
-          compute(std::true_type{}, base, stage, valid);
+          compute(std::true_type{}, careful, base, stage, valid);
         else
-          compute(std::false_type{}, base, stage, valid);
+          compute(std::false_type{}, std::false_type{}, base, stage, valid);
       }
       valid = next;
     }
+  };
+  walk(std::false_type{});
+  {
+    // a hidden infinity or NaN of V has spoilt the sums of its tile: once more, with
+    // an eye on those
+    float z = 0.0f;  // becomes NaN if any sum is not finite
+#pragma unroll
+    for (int d = 0; d < DV; ++d)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) z = fmaf(o[d][x], 0.0f, z);
+    if (__syncthreads_or(z != 0.0f)) walk(std::true_type{});
   }
 
   if (!in) return;

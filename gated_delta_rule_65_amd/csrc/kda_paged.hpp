@@ -73,7 +73,9 @@ struct AttnLaunch {
   float scale;
   int row_blocks;          // rows kernel: 16-row blocks per wave (1 or 2)
   int rows_limit;          // rows kernel: a request with more rows is the tiles kernel's
+  int by_request;          // rows kernel: a workgroup per request, not per row tile
   int rows_splits, tile_splits;
+  int rows_min_keys, tile_min_keys;  // keys per split at least
   int tile_waves;          // tiles kernel: waves of 32 rows, 0 = not launched
   void* stream;
 };

@@ -64,9 +64,8 @@ kda_status page_stride(const char* name, int64_t s, int64_t dense, size_t es, in
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The launch plan and its workspace.
+// The workspace of split partials.
 struct Plan {
-  int row_blocks, rows_limit, rows_splits, tile_waves, tile_splits;
   size_t o_bytes, lse_bytes, n_bytes;
 };
 
@@ -127,27 +126,32 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
     keys = (int64_t)L.window + L.sinks + most_new;
   // Requests of up to 32 rows per kv head, and every fp32 one, are the rows kernel's;
   // a request with more fills the matrix tiles.
-  const int64_t most_rows = most_new * L.group;
+  const int64_t most_rows = most_new * L.group, rows = a->total_tokens * a->hq;
   const bool tiles = a->dtype != KDA_F32 && most_rows > 32;
-  p.row_blocks = most_rows > 16 ? 2 : 1;
-  p.rows_limit = !tiles ? INT32_MAX : a->n > 1 ? 32 : 0;
-  p.tile_waves = tiles ? 8 : 0;
-  const int64_t rows = a->total_tokens * a->hq;
+  const bool few = !tiles || a->n > 1;
+  L.row_blocks = most_rows > 16 ? 2 : 1;
+  L.rows_limit = !tiles ? INT32_MAX : few ? 32 : 0;
+  L.by_request = most_rows <= 32 || tiles;
+  L.tile_waves = tiles ? 8 : 0;
   const int64_t cap = rows > 0 ? (int64_t)(MAX_PARTIALS / ((size_t)rows * a->head_dim * 4)) : 1;
-  auto splits_of = [&](int64_t base, int64_t wish, int64_t min_keys) {
-    int64_t want = a->splits > 0 ? a->splits : base > 0 ? ceil_div(wish, base) : 1;
-    if (a->splits == 0 && keys > 2048 && want < 4 && min_keys <= 256) want = 4;
+  // Splits: enough workgroups for every compute unit, and pieces of long visits small
+  // enough to even out ragged lengths, in a grid that the many unsplit requests do
+  // not swell.
+  auto splits_of = [&](int64_t base, int64_t least, int64_t grid) {
+    int64_t want = a->splits > 0 ? a->splits : base > 0 ? grid / base : 1;
     if (want > MAX_SPLITS) want = MAX_SPLITS;
-    if (want > ceil_div(keys, min_keys)) want = ceil_div(keys, min_keys);
+    if (want > ceil_div(keys, least)) want = ceil_div(keys, least);
     if (want > cap) want = cap;
     return want > 1 ? (int)want : 1;
   };
-  // Enough workgroups for every compute unit, and pieces of long visits small
-  // enough to even out ragged lengths.
-  p.rows_splits = p.rows_limit > 0 ? splits_of((int64_t)a->n * a->hkv, 1024, 256) : 1;
-  p.tile_splits = tiles ? splits_of(ceil_div(a->total_tokens * L.group, 32 * p.tile_waves) * a->hkv,
-                                    256, 512) : 1;
-  const int most = p.rows_splits > p.tile_splits ? p.rows_splits : p.tile_splits;
+  const int64_t units = L.by_request ? (int64_t)a->n * a->hkv
+                                     : (ceil_div(a->total_tokens * L.group, 16 * L.row_blocks)) * a->hkv;
+  L.rows_min_keys = units >= 256 ? 1024 : 256;
+  L.rows_splits = few ? splits_of(units, L.rows_min_keys, 16384) : 1;
+  L.tile_min_keys = 512;
+  L.tile_splits = tiles ? splits_of(ceil_div(a->total_tokens * L.group, 32 * L.tile_waves) * a->hkv,
+                                    L.tile_min_keys, 256) : 1;
+  const int most = L.rows_splits > L.tile_splits ? L.rows_splits : L.tile_splits;
   p.o_bytes = p.lse_bytes = p.n_bytes = 0;
   if (most > 1) {
     p.o_bytes = (size_t)most * rows * a->head_dim * 4;
@@ -275,12 +279,10 @@ KDA_API kda_status kda_paged_attention(const kda_paged_attention_args* a) {
     L.part_lse = (float*)(ws + p.o_bytes);
     L.part_n = (int32_t*)(ws + p.o_bytes + p.lse_bytes);
   }
-  L.row_blocks = p.row_blocks; L.rows_limit = p.rows_limit; L.rows_splits = p.rows_splits;
-  L.tile_waves = p.tile_waves; L.tile_splits = p.tile_splits;
   L.stream = a->stream;
   hipError_t e = hipSuccess;
-  if (p.tile_waves > 0) e = kda::launch_attn_tiles(L);
-  if (e == hipSuccess && p.rows_limit > 0) e = kda::launch_attn_rows(L);
+  if (L.tile_waves > 0) e = kda::launch_attn_tiles(L);
+  if (e == hipSuccess && L.rows_limit > 0) e = kda::launch_attn_rows(L);
   if (e == hipSuccess && need > 0) e = kda::launch_attn_join(L);
   if (e != hipSuccess) FAIL(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
   return (kda_status)kda::set_ok();
