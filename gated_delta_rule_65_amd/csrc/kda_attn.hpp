@@ -195,8 +195,9 @@ __device__ __forceinline__ int split_of(int tiles, int splits, int least, int& p
 struct PageWindow {
   const int32_t* row;
   int base, entry;
+  uint64_t none;  // lanes without a page
   __device__ __forceinline__ PageWindow(const AttnLaunch& a, int req)
-      : row(a.table + (int64_t)req * a.table_stride), base(-(1 << 30)), entry(-1) {}
+      : row(a.table + (int64_t)req * a.table_stride), base(-(1 << 30)), entry(-1), none(0) {}
   // Makes pages first .. last (both of the same tile) available; -1 where the
   // table has no valid page.  All arguments are wave-uniform.
   __device__ __forceinline__ void cover(const AttnLaunch& a, int first, int last, int lane) {
@@ -205,6 +206,11 @@ struct PageWindow {
     const int i = base + lane;
     const int e = i < a.max_pages ? row[i] : -1;
     entry = (uint32_t)e < (uint32_t)a.num_pages ? e : -1;
+    none = __ballot(entry < 0);
+  }
+  // Whether any of the pages first .. last is missing.
+  __device__ __forceinline__ bool missing(int first, int last) const {
+    return (none >> (first - base)) & (~0ull >> (63 - (last - first)));
   }
   __device__ __forceinline__ int at(int page) const {
     return __builtin_amdgcn_ds_bpermute(4 * (page - base), entry);

@@ -89,7 +89,7 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
 
     // this lane's rows (the MFMA columns l16 of each block): their queries, zero
     // past the last row, and their positions
-    uint4 q[RB][QS];
+    u32x4v_t q[RB][QS];
     int qpos[RB];
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
@@ -98,11 +98,16 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
       const int head = kvh * a.group + first + r - tok * a.group;
       qpos[b] = pos0 + tok;
       const bool in = r < rows;
-      const uint4* src = reinterpret_cast<const uint4*>(
+      const u32x4v_t* src = reinterpret_cast<const u32x4v_t*>(
           (const E*)a.q + (in ? (int64_t)(rt.start + tok) * a.q_stride + head * DIM : 0));
 #pragma unroll
-      for (int s = 0; s < QS; ++s) q[b][s] = in ? src[4 * s + gq] : make_uint4(0, 0, 0, 0);
+      for (int s = 0; s < QS; ++s) q[b][s] = in ? src[4 * s + gq] : u32x4v_t{0, 0, 0, 0};
     }
+    // they arrive here: a wait for them in the loop would wait for the DMA too
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int s = 0; s < QS; ++s) asm volatile("" : "+v"(q[b][s]));
 
     f32x4_t o[DIM / 16][RB];
     float m[RB], l[RB];
