@@ -45,6 +45,13 @@ __device__ __forceinline__ void dma16(const void* g, uint32_t lds) {
                : "s"(lds), "v"(g)
                : "memory", "m0");
 }
+// The same with a uniform base and a byte offset per lane.
+__device__ __forceinline__ void dma16(const char* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
 #pragma clang diagnostic pop
 // Waits until at most N of the wave's vector-memory operations are in flight.
 template <int N> __device__ __forceinline__ void dma_wait() {
@@ -214,6 +221,10 @@ struct PageWindow {
   }
   __device__ __forceinline__ int at(int page) const {
     return __builtin_amdgcn_ds_bpermute(4 * (page - base), entry);
+  }
+  // The same for a wave-uniform page.
+  __device__ __forceinline__ int uniform_at(int page) const {
+    return __builtin_amdgcn_readlane(entry, page - base);
   }
 };
 

@@ -2,20 +2,36 @@
 //
 // The same one-pass softmax as the rows kernel, with the work of a matrix product:
 // a workgroup holds 32 rows per wave and all its waves walk the keys together, 64
-// at a time, from K and V tiles in LDS that the next ones replace while they are
-// used.  S^T = K Q^T and O^T = V^T P^T run on 32 x 32 x 16 matrix instructions;
-// lane l holds row l % 32 of its wave, in S^T as in O^T, so a row's maximum and sum
-// take one swap between the wave's halves.
+// at a time, from K and V tiles in LDS.  S^T = K Q^T and O^T = V^T P^T run on
+// 32 x 32 x 16 matrix instructions; lane l holds row l % 32 of its wave, in S^T as in
+// O^T, so a row's maximum and sum take one swap between the wave's halves.
+//
+// Bound by the matrix cores and the vector unit together: a tile of 64 keys costs a
+// wave 32 products (1024 cycles for 128 channels) and about 240 vector instructions
+// with 32 exponentials (about as much), and a SIMD holds two waves (246 registers).
+// So the two have to be out of step, one multiplying while the other weighs:
+//  - They drift apart by themselves where barriers are rare and products go first
+//    (s_setprio).  2048 tokens on 131072 keys, 32 heads: 3.93 ms (1.11 PFLOP/s; 4.31
+//    ms in step, 4.46 ms with the phases held apart by barriers, 4.60 ms with one
+//    tile's products woven into the last one's softmax).
+//  - Fragment reads stay three ahead of their products (left to the compiler, each
+//    product waits for its own read: 5.9 ms).
+// Both shapes below have two waves per SIMD and 128 KB of LDS per compute unit.  Eight
+// waves (256 rows, two tiles a barrier) read each key half as often, which long visits
+// need; two workgroups of four waves (128 rows, a tile a barrier) even out ragged
+// requests (33 requests of 1 .. 700 tokens: 157 us against 184 us; 2048 tokens on
+// 131072 keys: 4.54 ms against 3.93 ms).
 #include "kda_attn.hpp"
 
 namespace kda {
 namespace {
 
 constexpr int KT = 64;    // keys per tile
-constexpr int RING = 4;   // tiles in LDS
 constexpr int MFMA = 0x8, DS_READ = 0x100;  // instruction classes of sched_group_barrier
 
-__device__ __forceinline__ int kswz(int r) { return r & 7; }
+// A fragment read takes one piece each of 16 consecutive rows at a time: they spread
+// over the 256 bytes of all banks.
+template <int P> __device__ __forceinline__ int kswz(int r) { return P == 16 ? r & 15 : (r >> 1) & 7; }
 // The transposing read takes 32 bytes of rows r .. r + 3 at two neighbouring
 // 32-byte columns per half wave: with this the eight fall into different banks.
 template <int P> __device__ __forceinline__ int vswz(int r) {
@@ -28,6 +44,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   constexpr int P = DIM / 8;            // 16-byte pieces per row
   constexpr int NI = P / NW > 0 ? P / NW : 1;  // DMA instructions per wave and tile
   constexpr int QS = DIM / 16, DV = DIM / 32;
+  constexpr int RING = NW / 2, PAIR = RING / 2;  // tiles in LDS, tiles per barrier
   static_assert(P % NW == 0, "a tile splits evenly over the waves");
   __shared__ uint4 smem[RING][2][KT * P];
 
@@ -57,7 +74,6 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   // positions of the wave's first and last row
   const int wa = pos0 + (int)fdiv(rt.first + 32 * wave, a.gdiv);
   const int wb = pos0 + (int)fdiv(rt.first + min(32 * wave + 31, rows - 1), a.gdiv);
-  const bool busy = 32 * wave < rows;
   frag q[QS];
   {
     const uint4* src = reinterpret_cast<const uint4*>(
@@ -72,10 +88,10 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
 
   // LDS byte addresses of the fragments in stage 0: key row l32 of a K tile, and the
   // rows and columns that this lane points the transposing reads at (both swizzles
-  // depend on the row modulo 8 alone, so the other rows are constants away)
+  // depend on the row modulo 16 alone, so the other rows are constants away)
   uint32_t ka[QS], va[DV];
 #pragma unroll
-  for (int x = 0; x < QS; ++x) ka[x] = lds_addr(&smem[0][0][l32 * P + ((2 * x + h) ^ kswz(l32))]);
+  for (int x = 0; x < QS; ++x) ka[x] = lds_addr(&smem[0][0][l32 * P + ((2 * x + h) ^ kswz<P>(l32))]);
 #pragma unroll
   for (int d = 0; d < DV; ++d) {
     const int i16 = lane & 15, row = 4 * h + (i16 >> 2);
@@ -92,6 +108,15 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   const char* const kbase = (const char*)a.kc + (int64_t)kvh * a.page.d * (DIM * 2);
   const char* const vbase = (const char*)a.vc + (int64_t)kvh * a.page.d * (DIM * 2);
 
+  // Byte offsets of this lane's pieces from the first of an instruction's keys (64 / P
+  // of them; the swizzles depend on the row modulo 16 alone, which is the same for
+  // every instruction of this wave), and whether those always share a page.
+  const int lrow = (64 * wave + lane) / P, lps = lane % P;
+  const uint32_t koff = lane / P * ROW + 16 * (lps ^ kswz<P>(lrow));
+  const uint32_t voff = lane / P * ROW + 16 * (lps ^ vswz<P>(lrow));
+  static_assert(NW * (64 / P) % 16 == 0, "a wave's rows agree modulo 16");
+  const bool even = a.page.d % (64 / P) == 0;
+
   // Issues the DMA of key tile i; returns which of its keys exist.
   auto issue = [&](int i, int stage) __attribute__((always_inline)) -> uint64_t {
     const int base = range.base(i);
@@ -105,15 +130,27 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
       const int key = base + lane;
       valid = __ballot(range.has(key) && pages.at((int)fdiv(key, a.page)) >= 0);
     }
+    if (even && valid == ~0ull) {
+      // one page per instruction: the addresses are scalar work
 #pragma unroll
+      for (int x = 0; x < NI; ++x) {
+        const int first = 64 * (wave + NW * x), key = base + first / P;
+        const int pg = (int)fdiv(key, a.page), off = key - pg * (int)a.page.d;
+        const int64_t page = pages.uniform_at(pg);
+        dma16(kbase + page * a.k_page + off * (DIM * 2), koff, lds_addr(&smem[stage][0][first]));
+        dma16(vbase + page * a.v_page + off * (DIM * 2), voff, lds_addr(&smem[stage][1][first]));
+      }
+      return valid;
+    }
+#pragma unroll 1
     for (int x = 0; x < NI; ++x) {
       const int first = 64 * (wave + NW * x);
-      const int slot = first + lane, row = slot / P, ps = slot % P;
+      const int slot = first + lane, row = slot / P;
       const int pg = (int)fdiv(base + row, a.page), off = base + row - pg * (int)a.page.d;
-      const int page = pages.at(pg);
-      const char* kp = kbase + (int64_t)page * a.k_page + off * (DIM * 2) + 16 * (ps ^ kswz(row));
-      const char* vp = vbase + (int64_t)page * a.v_page + off * (DIM * 2) + 16 * (ps ^ vswz<P>(row));
-      if (valid != ~0ull && !((valid >> row) & 1)) kp = vp = (const char*)&attn_zero;
+      const int64_t page = pages.at(pg);
+      const char* kp = kbase + page * a.k_page + (off - lane / P) * (DIM * 2) + koff;
+      const char* vp = vbase + page * a.v_page + (off - lane / P) * (DIM * 2) + voff;
+      if (!((valid >> row) & 1)) kp = vp = (const char*)&attn_zero;
       dma16(kp, lds_addr(&smem[stage][0][first]));
       dma16(vp, lds_addr(&smem[stage][1][first]));
     }
@@ -123,25 +160,48 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   f32x16_t s[2];
   frag p[4];
 
-  // S^T = K Q^T.  The scheduler is told to keep AHEAD fragment reads in flight: left
-  // to itself it waits for each one right before its product.
-  auto scores = [&](int stage) __attribute__((always_inline)) {
-    constexpr int AHEAD = 6, N = 2 * QS;
+  auto clear_scores = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int x = 0; x < 16; ++x) s[k][x] = 0.0f;
+  };
+  auto score = [&](int stage, int n) __attribute__((always_inline)) {  // S^T += K Q^T, step n
+    const int x = n / 2, k = n % 2;
+    s[k] = Half<E>::mma32(
+        __builtin_bit_cast(frag, lds_read16(ka[x] + stage * STAGE + 32 * k * ROW)), q[x], s[k]);
+  };
+  auto value = [&](int stage, int n) __attribute__((always_inline)) {  // O^T += V^T P^T, step n
+    const int kc = n / DV, d = n % DV;
+    const uint32_t at = va[d] + stage * STAGE + 16 * kc * ROW;
+    typedef short s16x8_t __attribute__((ext_vector_type(8)));
+    const s16x4_t u = lds_read_tr(at), w = lds_read_tr(at + 8 * ROW);
+    const s16x8_t z = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
+    o[d] = Half<E>::mma32(__builtin_bit_cast(frag, z), p[kc], o[d]);
+  };
+  // The products of a slot.  The scheduler is told to keep AHEAD fragments' reads in
+  // flight: left to itself it waits for each one right before its product.
+  constexpr int AHEAD = 3, NS = 2 * QS, NV = 4 * DV;
+  auto scores = [&](int stage) __attribute__((always_inline)) {
+    clear_scores();
 #pragma unroll
-    for (int x = 0; x < QS; ++x)
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        s[k] = Half<E>::mma32(
-            __builtin_bit_cast(frag, lds_read16(ka[x] + stage * STAGE + 32 * k * ROW)), q[x], s[k]);
+    for (int n = 0; n < NS; ++n) score(stage, n);
     __builtin_amdgcn_sched_group_barrier(DS_READ, AHEAD, 0);
 #pragma unroll
-    for (int x = 0; x < N - AHEAD; ++x) {
+    for (int n = 0; n < NS - AHEAD; ++n) {
       __builtin_amdgcn_sched_group_barrier(MFMA, 1, 0);
       __builtin_amdgcn_sched_group_barrier(DS_READ, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(MFMA, AHEAD, 0);
+  };
+  auto values = [&](int stage) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < NV; ++n) value(stage, n);
+    __builtin_amdgcn_sched_group_barrier(DS_READ, 2 * AHEAD, 0);
+#pragma unroll
+    for (int n = 0; n < NV - AHEAD; ++n) {
+      __builtin_amdgcn_sched_group_barrier(MFMA, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(DS_READ, 2, 0);
     }
     __builtin_amdgcn_sched_group_barrier(MFMA, AHEAD, 0);
   };
@@ -182,26 +242,6 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
         l += e;
         Half<E>::set(p[2 * k + x / 8], x % 8, e);
       }
-  };
-  auto values = [&](int stage) __attribute__((always_inline)) {  // O^T += V^T P^T
-    constexpr int AHEAD = 6, N = 4 * DV;
-#pragma unroll
-    for (int kc = 0; kc < 4; ++kc)
-#pragma unroll
-      for (int d = 0; d < DV; ++d) {
-        const uint32_t at = va[d] + stage * STAGE + 16 * kc * ROW;
-        typedef short s16x8_t __attribute__((ext_vector_type(8)));
-        const s16x4_t u = lds_read_tr(at), w = lds_read_tr(at + 8 * ROW);
-        const s16x8_t z = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
-        o[d] = Half<E>::mma32(__builtin_bit_cast(frag, z), p[kc], o[d]);
-      }
-    __builtin_amdgcn_sched_group_barrier(DS_READ, 2 * AHEAD, 0);
-#pragma unroll
-    for (int x = 0; x < N - AHEAD; ++x) {
-      __builtin_amdgcn_sched_group_barrier(MFMA, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(DS_READ, 2, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(MFMA, AHEAD, 0);
   };
   // The same on the vector unit, key by key, added where the key is visible: V may
   // hold infinities or NaN that some rows must not see (0 times them is NaN).
@@ -245,66 +285,48 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
 #pragma unroll
       for (int x = 0; x < 16; ++x) o[d][x] = 0.0f;
   };
-  // Whether any of the wave's rows sees a key of the tile, and whether all of them
-  // see all of it.
-  auto visible = [&](int base) __attribute__((always_inline)) {
-    return busy && base <= wb && !(a.window > 0 && base + KT - 1 <= wa - a.window && base >= a.sinks);
-  };
+  // Whether all of the wave's rows see all of the tile.
   auto whole = [&](int base, uint64_t valid) __attribute__((always_inline)) {
     return base + KT - 1 <= wa && valid == ~0ull &&
            !(a.window > 0 && base <= wb - a.window && base + KT > a.sinks);
   };
 
-  // The two waves of a SIMD take turns: while one is at its matrix products (O of the
-  // last tile, S of this one) the other is at its softmax, a barrier apart.  Slot
-  // 2 i: waves 0 .. 3 multiply for tile i, the others take the softmax of tile i - 1;
-  // slot 2 i + 1: the other way round.  Tile j is asked for in slots 2 j - 4 and
-  // 2 j - 3, the last reader of tile j - 4 was in slot 2 j - 5, and it has landed by
-  // slot 2 j.
+  // PAIR tiles between barriers, while the DMA fills the other half of the ring.
   auto walk = [&]() __attribute__((always_inline)) {
-    const bool late = wave >= NW / 2;
-    const int nt = t1 - t0;
     clear();
-    if (nt <= 0) return;
-    uint64_t v0 = ~0ull, v1 = ~0ull, v2 = ~0ull;  // the keys of tiles i, i + 1, i + 2
+    uint64_t valid[PAIR], next[PAIR];  // the keys of the tiles
+    auto load = [&](int i, int half) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < PAIR; ++j) {
+        next[j] = 0;
+        if (i + j < t1) next[j] = issue(i + j, half * PAIR + j);
+      }
+    };
+    load(t0, 0);
+    int half = 0;
 #pragma unroll 1
-    for (int i = 0; i < 2 && i < nt; ++i) {
-      v0 = v1;
-      v1 = issue(t0 + i, i);
-    }
-    if (nt == 1) v0 = v1;
-    dma_wait<0>();
-    __builtin_amdgcn_s_barrier();
-    if (late) __builtin_amdgcn_s_barrier();
-    bool live = false;  // P holds tile i - 1
-#pragma unroll 1
-    for (int i = 0; i < nt; ++i) {
-      const int base = range.base(t0 + i);
-      const bool vis = visible(base);
-      if (i + 2 < nt) v2 = issue(t0 + i + 2, (i + 2) % RING);
-      if (live) values((i + RING - 1) % RING);
-      if (vis) scores(i % RING);
+    for (int i = t0; i < t1; i += PAIR, half ^= 1) {
+#pragma unroll
+      for (int j = 0; j < PAIR; ++j) valid[j] = next[j];
+      // these tiles have landed for every wave, and every wave is done with the last
+      dma_wait<0>();
       lds_wait();
-      if (late) {
-        if (i + 2 < nt) dma_wait<2 * NI>();
-        else dma_wait<0>();
-      }
       __builtin_amdgcn_s_barrier();
-      if (vis) {
-        if (!whole(base, v0)) hide(base, v0);
+      load(i + PAIR, half ^ 1);
+#pragma unroll 1
+      for (int j = 0; j < PAIR && i + j < t1; ++j) {
+        const int base = range.base(i + j), stage = half * PAIR + j;
+        const uint64_t v = j == 0 ? valid[0] : valid[PAIR - 1];
+        __builtin_amdgcn_s_setprio(1);
+        scores(stage);
+        __builtin_amdgcn_s_setprio(0);
+        if (!whole(base, v)) hide(base, v);
         softmax();
+        __builtin_amdgcn_s_setprio(1);
+        values(stage);
+        __builtin_amdgcn_s_setprio(0);
       }
-      live = vis;
-      if (!late) {
-        if (i + 2 < nt) dma_wait<2 * NI>();
-        else dma_wait<0>();
-      }
-      v0 = v1;
-      v1 = v2;
-      __builtin_amdgcn_s_barrier();
     }
-    if (live) values((nt - 1) % RING);
-    if (!late) __builtin_amdgcn_s_barrier();
   };
   // The same tile by tile, with the hidden keys' values kept out of the sums.
   auto walk_carefully = [&]() __attribute__((always_inline)) {
@@ -316,7 +338,6 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
       const uint64_t valid = issue(i, 0);
       dma_wait<0>();
       __syncthreads();
-      if (!visible(base)) continue;
       scores(0);
       hide(base, valid);
       softmax();
@@ -367,7 +388,7 @@ template <typename E, int DIM, int NW> hipError_t tiles_go(const AttnLaunch& L) 
   return hipGetLastError();
 }
 template <typename E, int DIM> hipError_t tiles_nw(const AttnLaunch& L) {
-  return tiles_go<E, DIM, 8>(L);
+  return L.tile_waves == 8 ? tiles_go<E, DIM, 8>(L) : tiles_go<E, DIM, 4>(L);
 }
 template <typename E> hipError_t tiles_dim(const AttnLaunch& L) {
   return L.dim == 64 ? tiles_nw<E, 64>(L) : tiles_nw<E, 128>(L);

@@ -132,7 +132,10 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
   L.row_blocks = most_rows > 16 ? 2 : 1;
   L.rows_limit = !tiles ? INT32_MAX : few ? 32 : 0;
   L.by_request = most_rows <= 32 || tiles;
-  L.tile_waves = tiles ? 8 : 0;
+  // Eight waves (256 rows) a workgroup where key ranges are long and the rows fill the
+  // chip with them, else four: kda_attn_tiles.hip says why, with both sides measured.
+  const int64_t tile_rows = a->total_tokens * L.group;
+  L.tile_waves = !tiles ? 0 : keys >= 32768 && ceil_div(tile_rows, 256) * a->hkv >= 256 ? 8 : 4;
   const int64_t cap = rows > 0 ? (int64_t)(MAX_PARTIALS / ((size_t)rows * a->head_dim * 4)) : 1;
   // Splits: enough workgroups for every compute unit, and pieces of long visits small
   // enough to even out ragged lengths, in a grid that the many unsplit requests do
@@ -149,8 +152,8 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
   L.rows_min_keys = units >= 256 ? 1024 : 256;
   L.rows_splits = few ? splits_of(units, L.rows_min_keys, 16384) : 1;
   L.tile_min_keys = 512;
-  L.tile_splits = tiles ? splits_of(ceil_div(a->total_tokens * L.group, 32 * L.tile_waves) * a->hkv,
-                                    L.tile_min_keys, 256) : 1;
+  L.tile_splits = tiles ? splits_of(ceil_div(tile_rows, 32 * L.tile_waves) * a->hkv, L.tile_min_keys,
+                                    2048 / L.tile_waves) : 1;
   const int most = L.rows_splits > L.tile_splits ? L.rows_splits : L.tile_splits;
   p.o_bytes = p.lse_bytes = p.n_bytes = 0;
   if (most > 1) {
