@@ -20,9 +20,9 @@ namespace {
 
 constexpr int WAVES = 4;
 
-// Piece p of row r of a K tile sits in slot p ^ (r & 7) of the row (fragment reads
-// have 8 lanes take one piece each of 8 consecutive rows).
-__device__ __forceinline__ int kswz(int r) { return r & 7; }
+// Piece p of row r of a K tile sits in slot p ^ kswz(r) of the row: a fragment read
+// takes one piece each of the 16 rows, which spread over the 256 bytes of all banks.
+template <int P> __device__ __forceinline__ int kswz(int r) { return P >= 16 ? r : r >> 1; }
 // V tiles are read 4 (16-bit) or 1 (fp32) columns by row groups: the slots of
 // rows that one read touches together fall into different 32- (64-) byte columns.
 template <typename E, int P> __device__ __forceinline__ int vswz(int r) {
@@ -70,6 +70,8 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
     if constexpr (R::F32) return 0.0f;
     else return Half<E>::P_BIAS;
   }();
+  constexpr int ROWS = 64 / P, ROW = DIM * (int)sizeof(E);  // keys of a DMA instruction, bytes of one
+  const bool even = a.page.d % ROWS == 0;                   // whether those always share a page
   uint4* const my = smem + wave * 2 * R::STAGE;
   PageWindow pages(a, rt.req);
   const char* const kbase = (const char*)a.kc + (int64_t)kvh * a.page.d * (DIM * sizeof(E));
@@ -115,27 +117,41 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
     auto issue = [&](int i, int stage) {
       Tile t;
       t.base = range.base(i);
-      pages.cover(a, (int)fdiv(t.base, a.page),
-                  (int)fdiv(min(t.base + KT - 1, (int)a.key_capacity - 1), a.page), lane);
-      // lane l looks key l % KT up
-      const int key = t.base + lane % KT;
-      const int pg = (int)fdiv(key, a.page);
-      int page = pages.at(pg);
-      if (!range.has(key)) page = -1;
-      const int off = key - pg * (int)a.page.d;
-      t.valid = (uint32_t)__ballot(page >= 0) & ALL;
+      const int p0 = (int)fdiv(t.base, a.page);
+      const int p1 = (int)fdiv(min(t.base + KT - 1, (int)a.key_capacity - 1), a.page);
+      pages.cover(a, p0, p1, lane);
       uint4* const kt = my + stage * R::STAGE;
       uint4* const vt = kt + KT * P;
+      // inside the range and with every page there (the common case), all keys exist
+      t.valid = ALL;
+      if (t.base + KT > range.end || !(t.base >= range.lo || t.base + KT <= range.sink_end) ||
+          pages.missing(p0, p1)) {
+        const int key = t.base + l16;
+        t.valid = (uint32_t)__ballot(range.has(key) && pages.at((int)fdiv(key, a.page)) >= 0) & ALL;
+      }
+      if (even && t.valid == ALL) {
+        // one page per instruction: the addresses are scalar work
 #pragma unroll
+        for (int x = 0; x < NI; ++x) {
+          const int key = t.base + x * ROWS, pg = (int)fdiv(key, a.page);
+          const int off = key - pg * (int)a.page.d;
+          const int64_t page = pages.uniform_at(pg);
+          const int r = (64 * x + lane) / P, ps = lane % P;
+          dma16(kbase + page * a.k_page + off * ROW, lane / P * ROW + 16 * (ps ^ kswz<P>(r)),
+                lds_addr(kt + 64 * x));
+          dma16(vbase + page * a.v_page + off * ROW, lane / P * ROW + 16 * (ps ^ vswz<E, P>(r)),
+                lds_addr(vt + 64 * x));
+        }
+        return t;
+      }
+#pragma unroll 1
       for (int x = 0; x < NI; ++x) {
-        const int slot = 64 * x + lane, r = slot / P, ps = slot % P;
-        const int pr = __builtin_amdgcn_ds_bpermute(4 * r, page);
-        const int orow = __builtin_amdgcn_ds_bpermute(4 * r, off);
-        const char* kp = kbase + (int64_t)pr * a.k_page + orow * (DIM * (int)sizeof(E)) +
-                         16 * (ps ^ kswz(r));
-        const char* vp = vbase + (int64_t)pr * a.v_page + orow * (DIM * (int)sizeof(E)) +
-                         16 * (ps ^ vswz<E, P>(r));
-        if (pr < 0) kp = vp = (const char*)&attn_zero;
+        const int r = (64 * x + lane) / P, ps = lane % P, key = t.base + r;
+        const int pg = (int)fdiv(key, a.page), off = key - pg * (int)a.page.d;
+        const int64_t page = pages.at(pg);
+        const char* kp = kbase + page * a.k_page + off * ROW + 16 * (ps ^ kswz<P>(r));
+        const char* vp = vbase + page * a.v_page + off * ROW + 16 * (ps ^ vswz<E, P>(r));
+        if (!((t.valid >> r) & 1)) kp = vp = (const char*)&attn_zero;
         dma16(kp, lds_addr(kt + 64 * x));
         dma16(vp, lds_addr(vt + 64 * x));
       }
@@ -188,7 +204,7 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
       for (int b = 0; b < RB; ++b) s[b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < QS; ++i) {
-        const uint4 kf = kt[l16 * P + ((4 * i + gq) ^ kswz(l16))];
+        const uint4 kf = kt[l16 * P + ((4 * i + gq) ^ kswz<P>(l16))];
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
           if constexpr (R::F32) {

@@ -9,7 +9,6 @@ torch's current stream of the tensors' device.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import NamedTuple
 
@@ -59,6 +58,10 @@ class PagedAttentionArgs(ctypes.Structure):
     ]
 
 
+_SIZEOF_TABLES = ctypes.sizeof(PageTablesArgs)
+_SIZEOF_APPEND = ctypes.sizeof(KvAppendArgs)
+_SIZEOF_ATTENTION = ctypes.sizeof(PagedAttentionArgs)
+
 EXPORTS = ("kda_page_tables", "kda_kv_append", "kda_paged_attention_workspace_size",
            "kda_paged_attention")
 _lib = None
@@ -90,40 +93,58 @@ class PageTables(NamedTuple):
     pages_taken: torch.Tensor    # int32 [1]
 
 
+# The checks below format their messages only when they fail: a call's host time is
+# what a short decode step waits for.
+
+def _fail(msg, exc=ValueError):
+    raise exc(msg)
+
+
 def _on_gpu(dev):
-    _need(dev.type == "cuda", f"tensors must be on a GPU, got {dev}")
+    if dev.type != "cuda":
+        _fail(f"tensors must be on a GPU, got {dev}")
 
 
 def _same_device(dev, **tensors):
     for name, t in tensors.items():
-        _need(t is None or t.device == dev, f"{name} must be on {dev}")
+        if t is not None and t.device != dev:
+            _fail(f"{name} must be on {dev}")
 
 
-def _guard(dev):
-    """Makes the tensors' device current for the launch."""
+def _call(fn, args, dev):
+    """Runs a library call with the tensors' device current; raises on an error."""
     if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+        st = fn(ctypes.byref(args))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(ctypes.byref(args))
+    if st != KDA_OK:
+        _raise(_lib, st)
 
 
-def _int32(x, shape, name, dev):
-    _need(tuple(x.shape) == shape, f"{name} must have shape {list(shape)}")
-    if x.dtype != torch.int32:
-        _need(x.dtype == torch.int64, f"{name} must have dtype torch.int32 or torch.int64",
-              TypeError)
+def _int32(x, n, name, dev):
+    """A 1-D index tensor as a contiguous int32 one on dev."""
+    if x.dim() != 1 or x.shape[0] != n:
+        _fail(f"{name} must have shape [{n}]")
+    if x.dtype is torch.int32 and x.device == dev and x.is_contiguous():
+        return x
+    if x.dtype is not torch.int32 and x.dtype is not torch.int64:
+        _fail(f"{name} must have dtype torch.int32 or torch.int64", TypeError)
     return x.to(device=dev, dtype=torch.int32).contiguous()
 
 
 def _table(block_table, n):
     """(row stride, columns) of an int32 [n, max_pages] block table."""
-    _need(block_table.dim() == 2 and block_table.shape[0] == n,
-          f"block_table must be [{n}, max_pages]")
-    _need(block_table.dtype == torch.int32, "block_table must have dtype torch.int32", TypeError)
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        _fail(f"block_table must be [{n}, max_pages]")
+    if block_table.dtype is not torch.int32:
+        _fail("block_table must have dtype torch.int32", TypeError)
     cols = block_table.shape[1]
     if block_table.is_contiguous():
         return cols, cols
-    _need((cols == 1 or block_table.stride(1) == 1) and
-          (n == 1 or block_table.stride(0) >= cols), "block_table rows must be dense")
+    if not ((cols == 1 or block_table.stride(1) == 1) and
+            (n == 1 or block_table.stride(0) >= cols)):
+        _fail("block_table rows must be dense")
     return (cols if n == 1 else block_table.stride(0)), cols
 
 
@@ -143,12 +164,15 @@ def _page_stride(name, cache):
 
 
 def _pools(k_cache, v_cache, dtype, hkv, dim):
-    _need(k_cache.dim() == 4 and k_cache.shape[1] == hkv and k_cache.shape[3] == dim,
-          f"k_cache must be [pages, {hkv}, page_size, {dim}]")
-    _need(v_cache.shape == k_cache.shape, "v_cache must have k_cache's shape")
-    _need(k_cache.dtype == dtype and v_cache.dtype == dtype,
-          f"k_cache and v_cache must have dtype {dtype}", TypeError)
-    return _page_stride("k_cache", k_cache), _page_stride("v_cache", v_cache)
+    """(K page stride, V page stride, page size, pages) of the caches."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[1] != hkv or shape[3] != dim:
+        _fail(f"k_cache must be [pages, {hkv}, page_size, {dim}]")
+    if v_cache.shape != shape:
+        _fail("v_cache must have k_cache's shape")
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+        _fail(f"k_cache and v_cache must have dtype {dtype}", TypeError)
+    return (_page_stride("k_cache", k_cache), _page_stride("v_cache", v_cache), shape[2], shape[0])
 
 
 def page_tables(context_lens, new_lens, free_pages, block_table, page_size, num_pages,
@@ -162,21 +186,25 @@ def page_tables(context_lens, new_lens, free_pages, block_table, page_size, num_
     the cache.  max_tokens: room in the slot map, at least the step's new tokens (a
     captured step keeps its largest).  Returns a PageTables; ``out`` gives one to
     write into (its slot_mapping then sets max_tokens)."""
-    n = context_lens.shape[0] if context_lens.dim() == 1 else -1
-    _need(n >= 0, "context_lens must be [n]")
-    _need(free_pages.dim() == 1, "free_pages must be [F]")
+    if context_lens.dim() != 1:
+        _fail("context_lens must be [n]")
+    n = context_lens.shape[0]
+    if free_pages.dim() != 1:
+        _fail("free_pages must be [F]")
     stride, cols = _table(block_table, n)
-    _need(int(page_size) >= 1, "page_size must be >= 1")
+    page_size = int(page_size)
+    if page_size < 1:
+        _fail("page_size must be >= 1")
     dev = block_table.device
-    ctx = _int32(context_lens, (n,), "context_lens", dev)
-    new = _int32(new_lens, (n,), "new_lens", dev)
-    free = _int32(free_pages, (free_pages.shape[0],), "free_pages", dev)
+    ctx = _int32(context_lens, n, "context_lens", dev)
+    new = _int32(new_lens, n, "new_lens", dev)
+    free = _int32(free_pages, free_pages.shape[0], "free_pages", dev)
     if out is None:
-        _need(max_tokens is not None and int(max_tokens) >= 0,
-              "max_tokens is needed (the room for new tokens)")
+        if max_tokens is None or int(max_tokens) < 0:
+            _fail("max_tokens is needed (the room for new tokens)")
         tokens = int(max_tokens)
         ints = torch.empty(2 * n + 2 + tokens, dtype=torch.int32, device=dev)
-        cu, seq, taken, pos = torch.split(ints, [n + 1, n, 1, tokens])
+        cu, seq, taken, pos = ints.split_with_sizes((n + 1, n, 1, tokens))
         out = PageTables(cu, seq, torch.empty(tokens, dtype=torch.int64, device=dev), pos, taken)
     else:
         tokens = out.slot_mapping.shape[0]
@@ -187,22 +215,22 @@ def page_tables(context_lens, new_lens, free_pages, block_table, page_size, num_
                                    ("slot_mapping", out.slot_mapping, (tokens,), torch.int64),
                                    ("positions", out.positions, (tokens,), torch.int32),
                                    ("pages_taken", out.pages_taken, (1,), torch.int32)):
-            _need(tuple(t.shape) == shape, f"out.{name} must have shape {list(shape)}")
-            _need(t.dtype == dt, f"out.{name} must have dtype {dt}", TypeError)
-            _need(t.is_contiguous(), f"out.{name} must be contiguous")
-            _need(t.device == dev, f"out.{name} must be on {dev}")
+            if tuple(t.shape) != shape:
+                _fail(f"out.{name} must have shape {list(shape)}")
+            if t.dtype is not dt:
+                _fail(f"out.{name} must have dtype {dt}", TypeError)
+            if not t.is_contiguous():
+                _fail(f"out.{name} must be contiguous")
+            if t.device != dev:
+                _fail(f"out.{name} must be on {dev}")
     _on_gpu(dev)
-    lib = load_library()
-    with _guard(dev):
-        a = PageTablesArgs(
-            ctypes.sizeof(PageTablesArgs), ctx.data_ptr(), new.data_ptr(), free.data_ptr(),
-            block_table.data_ptr(), stride, n, free.shape[0], cols, int(page_size),
-            int(num_pages), tokens, out.slot_mapping.data_ptr(), out.positions.data_ptr(),
-            out.cu_seqlens.data_ptr(), out.seq_lens.data_ptr(), out.pages_taken.data_ptr(),
-            torch.cuda.current_stream(dev).cuda_stream)
-        st = lib.kda_page_tables(ctypes.byref(a))
-    if st != KDA_OK:
-        _raise(lib, st)
+    lib = _lib or load_library()
+    _call(lib.kda_page_tables, PageTablesArgs(
+        _SIZEOF_TABLES, ctx.data_ptr(), new.data_ptr(), free.data_ptr(), block_table.data_ptr(),
+        stride, n, free.shape[0], cols, page_size, int(num_pages), tokens,
+        out.slot_mapping.data_ptr(), out.positions.data_ptr(), out.cu_seqlens.data_ptr(),
+        out.seq_lens.data_ptr(), out.pages_taken.data_ptr(),
+        torch.cuda.current_stream(dev).cuda_stream), dev)
     return out
 
 
@@ -211,45 +239,68 @@ def kv_append(k, v, k_cache, v_cache, slot_mapping):
     [pages, Hkv, page_size, D], in place (kda_kv_append).  slot_mapping [T] int64
     holds distinct slots page * page_size + offset; one outside the cache (-1) skips
     its token.  k and v may be views of a fused projection."""
-    _need(k.dim() == 3, "k must be [T, Hkv, D]")
-    _need(v.shape == k.shape, "v must have k's shape")
-    _need(k.dtype in _DTYPES, f"unsupported dtype {k.dtype}", TypeError)
-    _need(v.dtype == k.dtype, "v must have k's dtype", TypeError)
-    T, hkv, dim = k.shape
-    kp, vp = _pools(k_cache, v_cache, k.dtype, hkv, dim)
-    _need(slot_mapping.dim() == 1 and slot_mapping.shape[0] == T, f"slot_mapping must have shape [{T}]")
-    _need(slot_mapping.dtype == torch.int64, "slot_mapping must have dtype torch.int64", TypeError)
-    _need(slot_mapping.is_contiguous(), "slot_mapping must be contiguous")
-    ks, vs = binding._token_stride("k", k, 2), binding._token_stride("v", v, 2)
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 3:
+        _fail("k must be [T, Hkv, D]")
+    if v.shape != shape:
+        _fail("v must have k's shape")
+    if dtype not in _DTYPES:
+        _fail(f"unsupported dtype {dtype}", TypeError)
+    if v.dtype is not dtype:
+        _fail("v must have k's dtype", TypeError)
+    T, hkv, dim = shape
+    kp, vp, page_size, pages = _pools(k_cache, v_cache, dtype, hkv, dim)
+    if slot_mapping.dim() != 1 or slot_mapping.shape[0] != T:
+        _fail(f"slot_mapping must have shape [{T}]")
+    if slot_mapping.dtype is not torch.int64:
+        _fail("slot_mapping must have dtype torch.int64", TypeError)
+    if not slot_mapping.is_contiguous():
+        _fail("slot_mapping must be contiguous")
+    ks, vs = _rows_stride("k", k), _rows_stride("v", v)
     dev = k.device
-    _same_device(dev, v=v, k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping)
+    if not (v.device == dev and k_cache.device == dev and v_cache.device == dev and
+            slot_mapping.device == dev):
+        _same_device(dev, v=v, k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping)
     _on_gpu(dev)
-    lib = load_library()
-    with _guard(dev):
-        a = KvAppendArgs(
-            ctypes.sizeof(KvAppendArgs), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), slot_mapping.data_ptr(), T, ks, vs, kp, vp, _DTYPES[k.dtype], hkv,
-            dim, k_cache.shape[2], k_cache.shape[0], torch.cuda.current_stream(dev).cuda_stream)
-        st = lib.kda_kv_append(ctypes.byref(a))
-    if st != KDA_OK:
-        _raise(lib, st)
+    lib = _lib or load_library()
+    _call(lib.kda_kv_append, KvAppendArgs(
+        _SIZEOF_APPEND, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        slot_mapping.data_ptr(), T, ks, vs, kp, vp, _DTYPES[dtype], hkv, dim, page_size, pages,
+        torch.cuda.current_stream(dev).cuda_stream), dev)
+
+
+def _rows_stride(name, t):
+    """Elements between the tokens of [T, H, D] rows, 0 when dense."""
+    if t.is_contiguous():
+        return 0
+    _, h, d = t.shape
+    st, sh, sd = t.stride()
+    if sd == 1 and (sh == d or h == 1) and st >= h * d:     # a slice of a projection
+        return st
+    return binding._token_stride(name, t, 2)
 
 
 def _attention_args(q, k_cache, v_cache, block_table, n, scale, window, sinks, max_new_len, splits):
-    _need(q.dim() == 3, "q must be [T, Hq, D]")
-    _need(q.dtype in _DTYPES, f"unsupported dtype {q.dtype}", TypeError)
-    T, hq, dim = q.shape
-    _need(k_cache.dim() == 4, "k_cache must be [pages, Hkv, page_size, D]")
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
+        _fail("q must be [T, Hq, D]")
+    if dtype not in _DTYPES:
+        _fail(f"unsupported dtype {dtype}", TypeError)
+    T, hq, dim = shape
+    if k_cache.dim() != 4:
+        _fail("k_cache must be [pages, Hkv, page_size, D]")
     hkv = k_cache.shape[1]
-    kp, vp = _pools(k_cache, v_cache, q.dtype, hkv, dim)
-    _need(hkv > 0 and hq % hkv == 0, f"Hq ({hq}) must be divisible by Hkv ({hkv})")
+    kp, vp, page_size, pages = _pools(k_cache, v_cache, dtype, hkv, dim)
+    if hkv < 1 or hq % hkv != 0:
+        _fail(f"Hq ({hq}) must be divisible by Hkv ({hkv})")
     stride, cols = _table(block_table, n)
-    _need(int(window) >= 0 and int(sinks) >= 0, "window and sinks must be >= 0")
+    window, sinks = int(window), int(sinks)
+    if window < 0 or sinks < 0:
+        _fail("window and sinks must be >= 0")
     return PagedAttentionArgs(
-        ctypes.sizeof(PagedAttentionArgs), None, None, None, None, None, None, None, None, None, 0,
-        T, binding._token_stride("q", q, 2), kp, vp, stride, _DTYPES[q.dtype], n, hq, hkv, dim,
-        k_cache.shape[2], k_cache.shape[0], cols, min(int(window), 1 << 30),
-        min(int(sinks), 1 << 30), int(max_new_len or 0), int(splits),
+        _SIZEOF_ATTENTION, None, None, None, None, None, None, None, None, None, 0, T,
+        _rows_stride("q", q), kp, vp, stride, _DTYPES[dtype], n, hq, hkv, dim, page_size, pages, cols,
+        min(window, 1 << 30), min(sinks, 1 << 30), int(max_new_len or 0), int(splits),
         float(dim ** -0.5 if scale is None else scale), None)
 
 
@@ -284,22 +335,25 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, scal
     splits: 0 lets the library cut long key ranges; else at most that many pieces.
     workspace: optional scratch of paged_attention_workspace_bytes(), for one call at
     a time.  Returns out [T, Hq, D], or (out, lse [T, Hq] fp32) with return_lse."""
-    n = cu_seqlens.shape[0] - 1 if cu_seqlens.dim() == 1 else -1
-    _need(n >= 0, "cu_seqlens must be [n + 1]")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        _fail("cu_seqlens must be [n + 1]")
+    n = cu_seqlens.shape[0] - 1
     a = _attention_args(q, k_cache, v_cache, block_table, n, scale, window, sinks, max_new_len,
                         splits)
     dev = q.device
-    cu = _int32(cu_seqlens, (n + 1,), "cu_seqlens", dev)
-    seq = _int32(seq_lens, (n,), "seq_lens", dev)
-    shape = tuple(q.shape)
+    cu = _int32(cu_seqlens, n + 1, "cu_seqlens", dev)
+    seq = _int32(seq_lens, n, "seq_lens", dev)
+    shape = q.shape
     if output is not None:
-        _need(tuple(output.shape) == shape, "output must have q's shape")
-        _need(output.dtype == q.dtype, "output must have q's dtype", TypeError)
+        _need(output.shape == shape, "output must have q's shape")
+        _need(output.dtype is q.dtype, "output must have q's dtype", TypeError)
         _need(output.is_contiguous(), "output must be contiguous")
     if lse is not None:
-        _need(tuple(lse.shape) == shape[:2], "lse must be [T, Hq]")
-        _need(lse.dtype == torch.float32, "lse must have dtype torch.float32", TypeError)
+        _need(lse.shape == shape[:2], "lse must be [T, Hq]")
+        _need(lse.dtype is torch.float32, "lse must have dtype torch.float32", TypeError)
         _need(lse.is_contiguous(), "lse must be contiguous")
+    if workspace is not None:
+        _need(workspace.is_contiguous(), "workspace must be contiguous")
     _same_device(dev, k_cache=k_cache, v_cache=v_cache, block_table=block_table, output=output,
                  lse=lse, workspace=workspace)
     _on_gpu(dev)
@@ -307,23 +361,20 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, scal
         output = torch.empty(shape, dtype=q.dtype, device=dev)
     if return_lse and lse is None:
         lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
-    lib = load_library()
-    with _guard(dev):
+    lib = _lib or load_library()
+    if workspace is None:
         nbytes = ctypes.c_size_t(0)
         st = lib.kda_paged_attention_workspace_size(ctypes.byref(a), ctypes.byref(nbytes))
         if st != KDA_OK:
             _raise(lib, st)
-        if workspace is None and nbytes.value:
+        if nbytes.value:
             workspace = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
-        if workspace is not None:
-            _need(workspace.is_contiguous(), "workspace must be contiguous")
-            a.workspace = workspace.data_ptr()
-            a.workspace_bytes = workspace.numel() * workspace.element_size()
-        a.q, a.k_cache, a.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
-        a.block_table, a.cu_seqlens, a.seq_lens = block_table.data_ptr(), cu.data_ptr(), seq.data_ptr()
-        a.out, a.lse = output.data_ptr(), None if lse is None else lse.data_ptr()
-        a.stream = torch.cuda.current_stream(dev).cuda_stream
-        st = lib.kda_paged_attention(ctypes.byref(a))
-    if st != KDA_OK:
-        _raise(lib, st)
+    if workspace is not None:
+        a.workspace = workspace.data_ptr()
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+    a.q, a.k_cache, a.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+    a.block_table, a.cu_seqlens, a.seq_lens = block_table.data_ptr(), cu.data_ptr(), seq.data_ptr()
+    a.out, a.lse = output.data_ptr(), None if lse is None else lse.data_ptr()
+    a.stream = torch.cuda.current_stream(dev).cuda_stream
+    _call(lib.kda_paged_attention, a, dev)
     return (output, lse) if return_lse else output
