@@ -68,6 +68,10 @@ __device__ __forceinline__ u32x4v_t lds_read16(uint32_t at) {
   return *(__attribute__((address_space(3))) const u32x4v_t*)(uintptr_t)at;
 }
 
+__device__ __forceinline__ float lds_read4(uint32_t at) {
+  return *(__attribute__((address_space(3))) const float*)(uintptr_t)at;
+}
+
 // The four 16-bit values of this lane's column: within 16 lanes, lane i points
 // at 4 elements of row i / 4 (columns 4 (i % 4) ..) and receives column i of the
 // 4 x 16 block.
@@ -191,11 +195,12 @@ template <int KT> struct KeyRange {
   __device__ __forceinline__ bool has(int t) const { return t < end && (t >= lo || t < sink_end); }
 };
 
-// Splits of a visit of `tiles` key tiles: at most `splits`, of at least `least`
-// tiles each; per = tiles of one split.
+// Splits of a visit of `tiles` key tiles: at most `splits`, of at least `least` tiles
+// each; per = tiles of one split.
 __device__ __forceinline__ int split_of(int tiles, int splits, int least, int& per) {
-  per = max(least, (tiles + splits - 1) / splits);
-  return max(1, (tiles + per - 1) / per);
+  const int n = max(1, min(splits, tiles / least));
+  per = (tiles + n - 1) / n;
+  return max(1, (tiles + max(per, 1) - 1) / max(per, 1));
 }
 
 // 64 consecutive entries of one block table row, one per lane.

@@ -37,9 +37,12 @@ template <typename E, int DIM, int RB> struct Rows {
   static constexpr int NI = KT * P / 64;               // DMA instructions per K or V tile
   static constexpr int QS = P / 4;                     // Q pieces per lane and row block
   static constexpr int STAGE = 2 * KT * P;             // pieces of a K and a V tile
+  // fp32 products take longer than a tile's way from memory: one buffer each for K and
+  // V, refilled as soon as it is read, leaves room for a second workgroup
+  static constexpr int STAGES = F32 ? 1 : 2;
   static constexpr int OS = DIM + 4;                   // floats per joined row (padded)
   static constexpr int JOIN = WAVES * 16 * RB * OS / 4;
-  static constexpr int PIECES = WAVES * 2 * STAGE > JOIN ? WAVES * 2 * STAGE : JOIN;
+  static constexpr int PIECES = WAVES * STAGES * STAGE > JOIN ? WAVES * STAGES * STAGE : JOIN;
 };
 
 // One key tile on its way: where it starts and which of its keys exist.
@@ -49,11 +52,11 @@ struct Tile {
 };
 
 template <typename E, int DIM, int RB, bool BY_REQUEST>
-__global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
+__global__ __launch_bounds__(256, 2) void rows_kernel(const AttnLaunch a) {
   using R = Rows<E, DIM, RB>;
   constexpr uint32_t ALL = 0xffffu;
   constexpr int KT = R::KT, P = R::P, NI = R::NI, QS = R::QS;
-  __shared__ uint4 smem[R::PIECES];
+  __shared__ __attribute__((aligned(1024))) uint4 smem[R::PIECES];
   __shared__ float sm_m[WAVES][16 * RB], sm_l[WAVES][16 * RB];
 
   const int lane = threadIdx.x & 63, wave = wave_of();
@@ -70,9 +73,20 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
     if constexpr (R::F32) return 0.0f;
     else return Half<E>::P_BIAS;
   }();
+  uint4* const my = smem + wave * R::STAGES * R::STAGE;
   constexpr int ROWS = 64 / P, ROW = DIM * (int)sizeof(E);  // keys of a DMA instruction, bytes of one
+  // this lane's piece of an instruction's keys, as bytes from the first of them
+  const uint32_t koff = lane / P * ROW + 16 * (lane % P ^ kswz<P>(lane / P));
+  const uint32_t voff = lane / P * ROW + 16 * (lane % P ^ vswz<E, P>(lane / P));
+  // LDS byte addresses of fragments in the first stage.  K: key l16, piece 4 i + gq.
+  // V, fp32: key 4 gq + e, column 16 d + l16; 16-bit, for the transposing read: columns
+  // 16 d + 4 (l16 % 4) .. of key 4 gq + l16 / 4.  i and d change bits of their own.
+  const uint32_t ka = lds_addr(my + l16 * P + (gq ^ kswz<P>(l16)));
+  const int vrow = R::F32 ? 4 * gq : 4 * gq + (l16 >> 2);
+  const int vpiece = R::F32 ? l16 >> 2 : (l16 & 3) >> 1;
+  const uint32_t va = lds_addr(my + KT * P + vrow * P + (vpiece ^ vswz<E, P>(vrow))) +
+                      (R::F32 ? 4 * (l16 & 3) : 8 * (l16 & 1));
   const bool even = a.page.d % ROWS == 0;                   // whether those always share a page
-  uint4* const my = smem + wave * 2 * R::STAGE;
   PageWindow pages(a, rt.req);
   const char* const kbase = (const char*)a.kc + (int64_t)kvh * a.page.d * (DIM * sizeof(E));
   const char* const vbase = (const char*)a.vc + (int64_t)kvh * a.page.d * (DIM * sizeof(E));
@@ -105,23 +119,17 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
 #pragma unroll
       for (int s = 0; s < QS; ++s) q[b][s] = in ? src[4 * s + gq] : u32x4v_t{0, 0, 0, 0};
     }
-    // they arrive here: a wait for them in the loop would wait for the DMA too
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-      for (int s = 0; s < QS; ++s) asm volatile("" : "+v"(q[b][s]));
 
     f32x4_t o[DIM / 16][RB];
     float m[RB], l[RB];
 
-    auto issue = [&](int i, int stage) {
+    // Where key tile i starts and which of its keys exist.
+    auto locate = [&](int i) __attribute__((always_inline)) {
       Tile t;
       t.base = range.base(i);
       const int p0 = (int)fdiv(t.base, a.page);
       const int p1 = (int)fdiv(min(t.base + KT - 1, (int)a.key_capacity - 1), a.page);
       pages.cover(a, p0, p1, lane);
-      uint4* const kt = my + stage * R::STAGE;
-      uint4* const vt = kt + KT * P;
       // inside the range and with every page there (the common case), all keys exist
       t.valid = ALL;
       if (t.base + KT > range.end || !(t.base >= range.lo || t.base + KT <= range.sink_end) ||
@@ -129,20 +137,30 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
         const int key = t.base + l16;
         t.valid = (uint32_t)__ballot(range.has(key) && pages.at((int)fdiv(key, a.page)) >= 0) & ALL;
       }
+      return t;
+    };
+    // Issues the DMA of its K rows or its V rows, or of both.
+    auto issue = [&](const Tile& t, int stage, bool k, bool v) __attribute__((always_inline)) {
+      uint4* const kt = my + stage * R::STAGE;
+      uint4* const vt = kt + KT * P;
       if (even && t.valid == ALL) {
         // one page per instruction: the addresses are scalar work
+        uint32_t ko = koff, vo = voff;
+        asm volatile("" : "+v"(ko), "+v"(vo));  // or every x would keep its registers
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
           const int key = t.base + x * ROWS, pg = (int)fdiv(key, a.page);
           const int off = key - pg * (int)a.page.d;
           const int64_t page = pages.uniform_at(pg);
-          const int r = (64 * x + lane) / P, ps = lane % P;
-          dma16(kbase + page * a.k_page + off * ROW, lane / P * ROW + 16 * (ps ^ kswz<P>(r)),
-                lds_addr(kt + 64 * x));
-          dma16(vbase + page * a.v_page + off * ROW, lane / P * ROW + 16 * (ps ^ vswz<E, P>(r)),
-                lds_addr(vt + 64 * x));
+          // (the swizzles are linear: that of row r0 + x ROWS is r0's xor that of x ROWS)
+          if (k)
+            dma16(kbase + page * a.k_page + off * ROW, ko ^ 16 * kswz<P>(x * ROWS),
+                  lds_addr(kt + 64 * x));
+          if (v)
+            dma16(vbase + page * a.v_page + off * ROW, vo ^ 16 * vswz<E, P>(x * ROWS),
+                  lds_addr(vt + 64 * x));
         }
-        return t;
+        return;
       }
 #pragma unroll 1
       for (int x = 0; x < NI; ++x) {
@@ -152,59 +170,59 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
         const char* kp = kbase + page * a.k_page + off * ROW + 16 * (ps ^ kswz<P>(r));
         const char* vp = vbase + page * a.v_page + off * ROW + 16 * (ps ^ vswz<E, P>(r));
         if (!((t.valid >> r) & 1)) kp = vp = (const char*)&attn_zero;
-        dma16(kp, lds_addr(kt + 64 * x));
-        dma16(vp, lds_addr(vt + 64 * x));
+        if (k) dma16(kp, lds_addr(kt + 64 * x));
+        if (v) dma16(vp, lds_addr(vt + 64 * x));
       }
-      return t;
     };
 
-    // O += P V key by key on the vector unit, added where the key is visible: for
-    // tiles whose V holds an infinity or a NaN that some rows must not see (0 times
-    // it is NaN).
+    // O += P V key by key on the vector unit, added where the key is visible: V may
+    // hold infinities or NaN that some rows must not see (0 times them is NaN).
     auto by_key = [&](const Tile& t, const uint4* vt, const f32x4_t (&s)[RB]) {
 #pragma unroll 1
       for (int j = 0; j < KT; ++j) {
         float p[RB];
+        uint32_t see[RB];  // all ones where the row sees the key
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
           float x = 0.0f;
 #pragma unroll
           for (int r = 0; r < 4; ++r) x = (j & 3) == r ? s[b][r] : x;
-          p[b] = __shfl(x, l16 + 16 * ((j >> 2) & 3));
+          p[b] = __shfl(x, l16 + 16 * (j >> 2));
+          see[b] = 0u - ((seen(a, t.base, qpos[b], t.valid) >> j) & 1);
         }
 #pragma unroll
         for (int d = 0; d < DIM / 16; ++d) {
-          float v[4];
+          __builtin_amdgcn_sched_barrier(0);  // few registers at a time
+          u32x4v_t v;
           if constexpr (R::F32) {
-            const f32x4_t x =
-                __builtin_bit_cast(f32x4_t, vt[j * P + ((4 * d + gq) ^ vswz<E, P>(j))]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = x[i];
+            v = __builtin_bit_cast(u32x4v_t, vt[j * P + ((4 * d + gq) ^ vswz<E, P>(j))]);
           } else {
-            const E* x = reinterpret_cast<const E*>(vt + j * P + ((2 * d + (gq >> 1)) ^ vswz<E, P>(j))) +
-                         4 * (gq & 1);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = to_f32(x[i]);
+            const uint2 u = *reinterpret_cast<const uint2*>(
+                reinterpret_cast<const char*>(vt + j * P + ((2 * d + (gq >> 1)) ^ vswz<E, P>(j))) +
+                8 * (gq & 1));
+            v = u32x4v_t{__float_as_uint(Half<E>::widen(u.x & 0xffffu)),
+                         __float_as_uint(Half<E>::widen(u.x >> 16)),
+                         __float_as_uint(Half<E>::widen(u.y & 0xffffu)),
+                         __float_as_uint(Half<E>::widen(u.y >> 16))};
           }
 #pragma unroll
-          for (int b = 0; b < RB; ++b) {
-            const bool see = (seen(a, t.base, qpos[b], t.valid) >> j) & 1;
+          for (int b = 0; b < RB; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[d][b][i] += see ? p[b] * v[i] : 0.0f;
-          }
+            for (int i = 0; i < 4; ++i)
+              o[d][b][i] = fmaf(p[b], __uint_as_float(v[i] & see[b]), o[d][b][i]);
         }
       }
     };
 
-    auto compute = [&](const Tile& t, int stage, bool careful) {
-      const uint4* const kt = my + stage * R::STAGE;
-      const uint4* const vt = kt + KT * P;
-      f32x4_t s[RB];
+    f32x4_t s[RB];
+    auto scores = [&](int stage) __attribute__((always_inline)) {  // S^T = K Q^T
+      uint32_t at = ka + stage * (R::STAGE * 16);
+      asm volatile("" : "+v"(at));  // or every step would keep its address
 #pragma unroll
       for (int b = 0; b < RB; ++b) s[b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < QS; ++i) {
-        const uint4 kf = kt[l16 * P + ((4 * i + gq) ^ kswz<P>(l16))];
+        const u32x4v_t kf = lds_read16(at ^ 64 * i);
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
           if constexpr (R::F32) {
@@ -219,6 +237,12 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
           }
         }
       }
+    };
+    // The softmax of the tile's scores, and `values` before V is read.
+    // CAREFUL keeps the values of hidden keys out of the sums.
+    auto weigh = [&](auto careful, const Tile& t, int stage, auto values) __attribute__((always_inline)) {
+      constexpr bool CAREFUL = decltype(careful)::value;
+      const uint4* const vt = my + stage * R::STAGE + KT * P;
       // keys hidden from some rows, or absent
       const bool mixed = pa != pb && (t.base + KT - 1 > pa ||
                                       (a.window > 0 && t.base <= pb - a.window && t.base + KT > a.sinks));
@@ -266,36 +290,27 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
           l[b] += p;
         }
       }
-      if (careful && mixed) {
-        bool bad = false;
-#pragma unroll 2
-        for (int x = 0; x < NI; ++x) {
-          const uint4 u = vt[64 * x + lane];
-          if constexpr (R::F32) {
-            const f32x4_t y = __builtin_bit_cast(f32x4_t, u);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) bad |= !(fabsf(y[e]) < __builtin_inff());
-          } else {
-            bad |= nonfinite16<E>(u) != 0;
-          }
-        }
-        if (__any(bad)) {
+      values();
+      if constexpr (CAREFUL) {
+        if (mixed) {
           by_key(t, vt, s);
           return;
         }
       }
       if constexpr (R::F32) {
-        const float* const vf = reinterpret_cast<const float*>(vt);
+        uint32_t at = va + stage * (R::STAGE * 16);
+        asm volatile("" : "+v"(at));
 #pragma unroll
-        for (int d = 0; d < DIM / 16; ++d)
+        for (int d = 0; d < DIM / 16; ++d) {
+          if (d % 2 == 0) __builtin_amdgcn_sched_barrier(0);  // few registers at a time
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int r = 4 * gq + e, col = 16 * d + l16;
-            const float x = vf[r * DIM + (((col >> 2) ^ vswz<E, P>(r)) << 2) + (col & 3)];
+            const float x = lds_read4((at ^ 64 * d) + e * ROW);
 #pragma unroll
             for (int b = 0; b < RB; ++b)
               o[d][b] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, s[b][e], o[d][b], 0, 0, 0);
           }
+        }
       } else {
         // P^T as it lies: lane group gq holds keys 4 gq + r
         typename Half<E>::quad p[RB];
@@ -303,11 +318,10 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
         for (int b = 0; b < RB; ++b)
 #pragma unroll
           for (int r = 0; r < 4; ++r) Half<E>::set(p[b], r, s[b][r]);
+        const uint32_t at = va + stage * (R::STAGE * 16);
 #pragma unroll
         for (int d = 0; d < DIM / 16; ++d) {
-          // columns 16 d + 4 (l16 % 4) .. of row 4 gq + l16 / 4
-          const int r = 4 * gq + (l16 >> 2), piece = 2 * d + ((l16 & 3) >> 1);
-          const s16x4_t v = lds_read_tr(lds_addr(vt + r * P + (piece ^ vswz<E, P>(r))) + 8 * (l16 & 1));
+          const s16x4_t v = lds_read_tr(at ^ 32 * d);
 #pragma unroll
           for (int b = 0; b < RB; ++b) o[d][b] = Half<E>::mma16k16(v, p[b], o[d][b]);
         }
@@ -317,9 +331,7 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
     // contiguous tiles per wave
     const int share = (nt + WAVES - 1) / WAVES;
     const int w0 = t0 + min(nt, wave * share), w1 = t0 + min(nt, (wave + 1) * share);
-    // The second, careful pass is for waves whose sums met an infinity or a NaN.
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
+    auto walk = [&](auto careful) __attribute__((always_inline)) {
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
         m[b] = NEG_INF;
@@ -327,33 +339,67 @@ __global__ __launch_bounds__(256) void rows_kernel(const AttnLaunch a) {
 #pragma unroll
         for (int d = 0; d < DIM / 16; ++d) o[d][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
-      if (w0 < w1) {
-        Tile cur = issue(w0, 0);
+      if (w0 >= w1) return;
+      Tile cur = locate(w0);
+      if constexpr (R::STAGES == 2) {
+        issue(cur, 0, true, true);
+      } else {
+        issue(cur, 0, true, false);
+        issue(cur, 0, false, true);
+      }
+      // the queries arrive here: a wait for them in the loop would wait for the DMA too
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int x = 0; x < QS; ++x) asm volatile("" : "+v"(q[b][x]));
 #pragma unroll 1
-        for (int i = w0; i < w1; ++i) {
+      for (int i = w0; i < w1; ++i) {
+        const bool more = i + 1 < w1;
+        Tile next = cur;
+        if constexpr (R::STAGES == 2) {
           const int stage = (i - w0) & 1;
-          Tile next = cur;
-          if (i + 1 < w1) {
+          if (more) {
             lds_wait();  // the reads of the tile that this one replaces
-            next = issue(i + 1, stage ^ 1);
+            next = locate(i + 1);
+            issue(next, stage ^ 1, true, true);
             dma_wait<2 * NI>();
           } else {
             dma_wait<0>();
           }
-          compute(cur, stage, pass > 0);
-          cur = next;
+          scores(stage);
+          weigh(careful, cur, stage, [] {});
+        } else {
+          dma_wait<NI>();  // K of this tile; V may still be on its way
+          scores(0);
+          lds_wait();
+          if (more) {
+            next = locate(i + 1);
+            issue(next, 0, true, false);
+          }
+          weigh(careful, cur, 0, [&] {
+            if (more) dma_wait<NI>();
+            else dma_wait<0>();
+          });
+          lds_wait();
+          if (more) issue(next, 0, false, true);
         }
+        cur = next;
       }
-      if (pa == pb) break;  // every key of a tile is visible to all rows
-      float z = 0.0f;       // becomes NaN if any sum is not finite
+    };
+    walk(std::false_type{});
+    if (pa != pb) {  // else every key of a tile is visible to all rows
+      // a hidden infinity or NaN of V has spoilt the sums of its tile: once more, carefully
+      float z = 0.0f;  // becomes NaN if any sum is not finite
 #pragma unroll
       for (int b = 0; b < RB; ++b)
 #pragma unroll
         for (int d = 0; d < DIM / 16; ++d)
 #pragma unroll
           for (int r = 0; r < 4; ++r) z = fmaf(o[d][b][r], 0.0f, z);
-      if (!__any(z != 0.0f)) break;
-      lds_wait();
+      if (__any(z != 0.0f)) {
+        lds_wait();
+        walk(std::true_type{});
+      }
     }
 
     // join of the four waves
@@ -493,7 +539,8 @@ template <typename E> hipError_t rows_dim(const AttnLaunch& L) {
 }
 
 // Four waves share a row where there are many splits of few rows; with many rows,
-// most of which were not split, a wave looks at 16 of them.
+// most of which were not split, a wave looks at several of them: 16 where only the
+// rows kernel cuts (its rows are few), 4 where the tiles kernel does.
 template <typename E, int DIM> hipError_t join_go(const AttnLaunch& L) {
   const int splits = L.rows_splits > L.tile_splits ? L.rows_splits : L.tile_splits;
   const int64_t rows = (int64_t)L.total * L.hq;
@@ -501,7 +548,7 @@ template <typename E, int DIM> hipError_t join_go(const AttnLaunch& L) {
     hipLaunchKernelGGL((join_kernel<E, DIM, 4>), dim3((unsigned)rows), dim3(256), 0,
                        (hipStream_t)L.stream, L, splits, 1);
   } else {
-    const int each = rows <= 16384 ? 1 : 16;
+    const int each = rows <= 16384 ? 1 : L.tile_splits > 1 ? 4 : 16;
     hipLaunchKernelGGL((join_kernel<E, DIM, 1>), dim3((unsigned)((rows + 4 * each - 1) / (4 * each))),
                        dim3(256), 0, (hipStream_t)L.stream, L, splits, each);
   }

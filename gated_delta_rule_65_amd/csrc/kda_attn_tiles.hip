@@ -46,7 +46,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   constexpr int QS = DIM / 16, DV = DIM / 32;
   constexpr int RING = NW / 2, PAIR = RING / 2;  // tiles in LDS, tiles per barrier
   static_assert(P % NW == 0, "a tile splits evenly over the waves");
-  __shared__ uint4 smem[RING][2][KT * P];
+  __shared__ uint4 smem_k[RING][KT * P], smem_v[RING][KT * P];
 
   const int lane = threadIdx.x & 63, wave = wave_of();
   const int l32 = lane & 31, h = lane >> 5;
@@ -81,9 +81,6 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
 #pragma unroll
     for (int s = 0; s < QS; ++s)
       q[s] = __builtin_bit_cast(frag, in ? src[2 * s + h] : make_uint4(0, 0, 0, 0));
-    // they arrive here: a wait for them in the loop would wait for the DMA too
-#pragma unroll
-    for (int s = 0; s < QS; ++s) asm volatile("" : "+v"(q[s]));
   }
 
   // LDS byte addresses of the fragments in stage 0: key row l32 of a K tile, and the
@@ -91,14 +88,14 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   // depend on the row modulo 16 alone, so the other rows are constants away)
   uint32_t ka[QS], va[DV];
 #pragma unroll
-  for (int x = 0; x < QS; ++x) ka[x] = lds_addr(&smem[0][0][l32 * P + ((2 * x + h) ^ kswz<P>(l32))]);
+  for (int x = 0; x < QS; ++x) ka[x] = lds_addr(&smem_k[0][l32 * P + ((2 * x + h) ^ kswz<P>(l32))]);
 #pragma unroll
   for (int d = 0; d < DV; ++d) {
     const int i16 = lane & 15, row = 4 * h + (i16 >> 2);
     const int piece = 4 * d + 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
-    va[d] = lds_addr(&smem[0][1][row * P + (piece ^ vswz<P>(row))]) + 8 * (i16 & 1);
+    va[d] = lds_addr(&smem_v[0][row * P + (piece ^ vswz<P>(row))]) + 8 * (i16 & 1);
   }
-  constexpr int STAGE = 2 * KT * P * 16, ROW = P * 16;  // bytes
+  constexpr int STAGE = KT * P * 16, ROW = P * 16;  // bytes
 
   f32x16_t o[DV];
   float m, l;
@@ -137,8 +134,8 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
         const int first = 64 * (wave + NW * x), key = base + first / P;
         const int pg = (int)fdiv(key, a.page), off = key - pg * (int)a.page.d;
         const int64_t page = pages.uniform_at(pg);
-        dma16(kbase + page * a.k_page + off * (DIM * 2), koff, lds_addr(&smem[stage][0][first]));
-        dma16(vbase + page * a.v_page + off * (DIM * 2), voff, lds_addr(&smem[stage][1][first]));
+        dma16(kbase + page * a.k_page + off * (DIM * 2), koff, lds_addr(&smem_k[stage][first]));
+        dma16(vbase + page * a.v_page + off * (DIM * 2), voff, lds_addr(&smem_v[stage][first]));
       }
       return valid;
     }
@@ -151,8 +148,8 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
       const char* kp = kbase + page * a.k_page + (off - lane / P) * (DIM * 2) + koff;
       const char* vp = vbase + page * a.v_page + (off - lane / P) * (DIM * 2) + voff;
       if (!((valid >> row) & 1)) kp = vp = (const char*)&attn_zero;
-      dma16(kp, lds_addr(&smem[stage][0][first]));
-      dma16(vp, lds_addr(&smem[stage][1][first]));
+      dma16(kp, lds_addr(&smem_k[stage][first]));
+      dma16(vp, lds_addr(&smem_v[stage][first]));
     }
     return valid;
   };
@@ -246,7 +243,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   // The same on the vector unit, key by key, added where the key is visible: V may
   // hold infinities or NaN that some rows must not see (0 times them is NaN).
   auto values_by_key = [&](int base, int stage, uint64_t valid) __attribute__((always_inline)) {
-    const uint4* const vt = smem[stage][1];
+    const uint4* const vt = smem_v[stage];
 #pragma unroll 1
     for (int j = 0; j < KT; ++j) {
       // p of key j lies in slot e of chunk j / 16, in half (j / 4) % 2 of the wave
@@ -291,6 +288,14 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
            !(a.window > 0 && base <= wb - a.window && base + KT > a.sinks);
   };
 
+  // The fragment addresses move between the halves of the ring, so that within one
+  // every read's place is a constant.
+  auto turn = [&](int by) __attribute__((always_inline)) {
+#pragma unroll
+    for (int x = 0; x < QS; ++x) ka[x] += by;
+#pragma unroll
+    for (int d = 0; d < DV; ++d) va[d] += by;
+  };
   // PAIR tiles between barriers, while the DMA fills the other half of the ring.
   auto walk = [&]() __attribute__((always_inline)) {
     clear();
@@ -303,6 +308,9 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
       }
     };
     load(t0, 0);
+    // the queries arrive here: a wait for them in the loop would wait for the DMA too
+#pragma unroll
+    for (int x = 0; x < QS; ++x) asm volatile("" : "+v"(q[x]));
     int half = 0;
 #pragma unroll 1
     for (int i = t0; i < t1; i += PAIR, half ^= 1) {
@@ -313,20 +321,22 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
       lds_wait();
       __builtin_amdgcn_s_barrier();
       load(i + PAIR, half ^ 1);
-#pragma unroll 1
-      for (int j = 0; j < PAIR && i + j < t1; ++j) {
-        const int base = range.base(i + j), stage = half * PAIR + j;
-        const uint64_t v = j == 0 ? valid[0] : valid[PAIR - 1];
+#pragma unroll
+      for (int j = 0; j < PAIR; ++j) {
+        if (i + j >= t1) break;
+        const int base = range.base(i + j);
         __builtin_amdgcn_s_setprio(1);
-        scores(stage);
+        scores(j);
         __builtin_amdgcn_s_setprio(0);
-        if (!whole(base, v)) hide(base, v);
+        if (!whole(base, valid[j])) hide(base, valid[j]);
         softmax();
         __builtin_amdgcn_s_setprio(1);
-        values(stage);
+        values(j);
         __builtin_amdgcn_s_setprio(0);
       }
+      turn(half ? -PAIR * STAGE : PAIR * STAGE);
     }
+    if (half) turn(-PAIR * STAGE);
   };
   // The same tile by tile, with the hidden keys' values kept out of the sums.
   auto walk_carefully = [&]() __attribute__((always_inline)) {

@@ -137,23 +137,27 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
   const int64_t tile_rows = a->total_tokens * L.group;
   L.tile_waves = !tiles ? 0 : keys >= 32768 && ceil_div(tile_rows, 256) * a->hkv >= 256 ? 8 : 4;
   const int64_t cap = rows > 0 ? (int64_t)(MAX_PARTIALS / ((size_t)rows * a->head_dim * 4)) : 1;
-  // Splits: enough workgroups for every compute unit, and pieces of long visits small
-  // enough to even out ragged lengths, in a grid that the many unsplit requests do
-  // not swell.
+  // Splits: pieces of long visits small enough to even out ragged lengths and to give
+  // every compute unit work, in a grid of about `grid` workgroups, so that the many
+  // requests that are not split do not swell it.
   auto splits_of = [&](int64_t base, int64_t least, int64_t grid) {
     int64_t want = a->splits > 0 ? a->splits : base > 0 ? grid / base : 1;
     if (want > MAX_SPLITS) want = MAX_SPLITS;
-    if (want > ceil_div(keys, least)) want = ceil_div(keys, least);
+    if (want > keys / least) want = keys / least;
     if (want > cap) want = cap;
     return want > 1 ? (int)want : 1;
   };
   const int64_t units = L.by_request ? (int64_t)a->n * a->hkv
-                                     : (ceil_div(a->total_tokens * L.group, 16 * L.row_blocks)) * a->hkv;
-  L.rows_min_keys = units >= 256 ? 1024 : 256;
-  L.rows_splits = few ? splits_of(units, L.rows_min_keys, 16384) : 1;
-  L.tile_min_keys = 512;
-  L.tile_splits = tiles ? splits_of(ceil_div(tile_rows, 32 * L.tile_waves) * a->hkv, L.tile_min_keys,
-                                    2048 / L.tile_waves) : 1;
+                                     : ceil_div(a->total_tokens * L.group, 16 * L.row_blocks) * a->hkv;
+  L.rows_min_keys = units >= 1024 ? 2048 : units >= 256 ? 1024 : 256;
+  L.rows_splits = few ? splits_of(units, L.rows_min_keys, L.by_request ? 16384 : 2048) : 1;
+  // A split row costs the tiles kernel its fp32 partials, so they are cut only where
+  // there are few of them for the chip, counting ragged requests as fewer.
+  const int64_t tile_units = tiles ? ceil_div(tile_rows, 32 * L.tile_waves) * a->hkv : 0;
+  const int64_t enough = (L.tile_waves == 8 ? 256 : 512) * (a->n > 1 ? 3 : 1);
+  L.tile_min_keys = tile_units >= 256 ? 1024 : 512;
+  L.tile_splits = tiles && (a->splits > 0 || tile_units < enough)
+                      ? splits_of(tile_units, L.tile_min_keys, tile_units >= 256 ? 8192 : 1024) : 1;
   const int most = L.rows_splits > L.tile_splits ? L.rows_splits : L.tile_splits;
   p.o_bytes = p.lse_bytes = p.n_bytes = 0;
   if (most > 1) {
