@@ -203,31 +203,37 @@ __device__ __forceinline__ int split_of(int tiles, int splits, int least, int& p
   return max(1, (tiles + max(per, 1) - 1) / max(per, 1));
 }
 
-// 64 consecutive entries of one block table row, one per lane.
+// 64 consecutive entries of one block table row, one per lane.  Everything but `entry`
+// is wave-uniform.
 struct PageWindow {
   const int32_t* row;
   int base, entry;
-  uint64_t none;  // lanes without a page
+  int first_key, end_key;  // the keys of its pages
+  uint64_t none;           // lanes without a page
   __device__ __forceinline__ PageWindow(const AttnLaunch& a, int req)
-      : row(a.table + (int64_t)req * a.table_stride), base(-(1 << 30)), entry(-1), none(0) {}
-  // Makes pages first .. last (both of the same tile) available; -1 where the
-  // table has no valid page.  All arguments are wave-uniform.
+      : row(a.table + (int64_t)req * a.table_stride), base(0), entry(-1), first_key(0), end_key(0),
+        none(0) {}
+  // Makes the pages of the keys first .. last available (at most 64 of them).
   __device__ __forceinline__ void cover(const AttnLaunch& a, int first, int last, int lane) {
-    if (first >= base && last < base + 64) return;
-    base = first;
+    if (first >= first_key && last < end_key) return;
+    base = (int)fdiv(first, a.page);
     const int i = base + lane;
     const int e = i < a.max_pages ? row[i] : -1;
     entry = (uint32_t)e < (uint32_t)a.num_pages ? e : -1;
     none = __ballot(entry < 0);
+    first_key = base * (int)a.page.d;
+    end_key = (int)min((int64_t)(base + 64) * a.page.d, (int64_t)INT32_MAX);
   }
-  // Whether any of the pages first .. last is missing.
-  __device__ __forceinline__ bool missing(int first, int last) const {
-    return (none >> (first - base)) & (~0ull >> (63 - (last - first)));
+  // Whether any of the keys first .. last lies on no page.
+  __device__ __forceinline__ bool missing(const AttnLaunch& a, int first, int last) const {
+    if (none == 0) return false;
+    const int p0 = (int)fdiv(first, a.page), p1 = (int)fdiv(last, a.page);
+    return (none >> (p0 - base)) & (~0ull >> (63 - (p1 - p0)));
   }
+  // The page at index `page` of the row (a lane's own, or a uniform one), -1 if none.
   __device__ __forceinline__ int at(int page) const {
     return __builtin_amdgcn_ds_bpermute(4 * (page - base), entry);
   }
-  // The same for a wave-uniform page.
   __device__ __forceinline__ int uniform_at(int page) const {
     return __builtin_amdgcn_readlane(entry, page - base);
   }

@@ -127,13 +127,12 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(const AttnLaunch a) {
     auto locate = [&](int i) __attribute__((always_inline)) {
       Tile t;
       t.base = range.base(i);
-      const int p0 = (int)fdiv(t.base, a.page);
-      const int p1 = (int)fdiv(min(t.base + KT - 1, (int)a.key_capacity - 1), a.page);
-      pages.cover(a, p0, p1, lane);
+      const int last = min(t.base + KT - 1, (int)a.key_capacity - 1);
+      pages.cover(a, t.base, last, lane);
       // inside the range and with every page there (the common case), all keys exist
       t.valid = ALL;
       if (t.base + KT > range.end || !(t.base >= range.lo || t.base + KT <= range.sink_end) ||
-          pages.missing(p0, p1)) {
+          pages.missing(a, t.base, last)) {
         const int key = t.base + l16;
         t.valid = (uint32_t)__ballot(range.has(key) && pages.at((int)fdiv(key, a.page)) >= 0) & ALL;
       }
@@ -150,8 +149,7 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(const AttnLaunch a) {
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
           const int key = t.base + x * ROWS, pg = (int)fdiv(key, a.page);
-          const int off = key - pg * (int)a.page.d;
-          const int64_t page = pages.uniform_at(pg);
+          const int64_t off = key - pg * (int)a.page.d, page = pages.uniform_at(pg);
           // (the swizzles are linear: that of row r0 + x ROWS is r0's xor that of x ROWS)
           if (k)
             dma16(kbase + page * a.k_page + off * ROW, ko ^ 16 * kswz<P>(x * ROWS),
@@ -165,8 +163,8 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(const AttnLaunch a) {
 #pragma unroll 1
       for (int x = 0; x < NI; ++x) {
         const int r = (64 * x + lane) / P, ps = lane % P, key = t.base + r;
-        const int pg = (int)fdiv(key, a.page), off = key - pg * (int)a.page.d;
-        const int64_t page = pages.at(pg);
+        const int pg = (int)fdiv(key, a.page);
+        const int64_t off = key - pg * (int)a.page.d, page = pages.at(pg);
         const char* kp = kbase + page * a.k_page + off * ROW + 16 * (ps ^ kswz<P>(r));
         const char* vp = vbase + page * a.v_page + off * ROW + 16 * (ps ^ vswz<E, P>(r));
         if (!((t.valid >> r) & 1)) kp = vp = (const char*)&attn_zero;

@@ -114,16 +114,19 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   static_assert(NW * (64 / P) % 16 == 0, "a wave's rows agree modulo 16");
   const bool even = a.page.d % (64 / P) == 0;
 
-  // Issues the DMA of key tile i; returns which of its keys exist.
-  auto issue = [&](int i, int stage) __attribute__((always_inline)) -> uint64_t {
-    const int base = range.base(i);
-    const int p0 = (int)fdiv(base, a.page);
-    const int p1 = (int)fdiv(min(base + KT - 1, (int)a.key_capacity - 1), a.page);
-    pages.cover(a, p0, p1, lane);
+  // The page that this wave's DMA is in: its first key, and where its rows of this
+  // head begin (scalar values, kept from one instruction to the next).
+  int page_key = -(1 << 30);
+  const char *kpage = nullptr, *vpage = nullptr;
+
+  // Issues the DMA of the key tile at `base`; returns which of its keys exist.
+  auto issue = [&](int base, int stage) __attribute__((always_inline)) -> uint64_t {
+    const int last = min(base + KT - 1, (int)a.key_capacity - 1);
+    pages.cover(a, base, last, lane);
     // inside the range and with every page there (the common case), all keys exist
     uint64_t valid = ~0ull;
     if (base + KT > range.end || !(base >= range.lo || base + KT <= range.sink_end) ||
-        pages.missing(p0, p1)) {
+        pages.missing(a, base, last)) {
       const int key = base + lane;
       valid = __ballot(range.has(key) && pages.at((int)fdiv(key, a.page)) >= 0);
     }
@@ -132,10 +135,16 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
 #pragma unroll
       for (int x = 0; x < NI; ++x) {
         const int first = 64 * (wave + NW * x), key = base + first / P;
-        const int pg = (int)fdiv(key, a.page), off = key - pg * (int)a.page.d;
-        const int64_t page = pages.uniform_at(pg);
-        dma16(kbase + page * a.k_page + off * (DIM * 2), koff, lds_addr(&smem_k[stage][first]));
-        dma16(vbase + page * a.v_page + off * (DIM * 2), voff, lds_addr(&smem_v[stage][first]));
+        if ((uint32_t)(key - page_key) >= a.page.d) {
+          const int pg = (int)fdiv(key, a.page);
+          const int64_t page = pages.uniform_at(pg);
+          page_key = pg * (int)a.page.d;
+          kpage = kbase + page * a.k_page;
+          vpage = vbase + page * a.v_page;
+        }
+        const int64_t off = (int64_t)(key - page_key) * ROW;
+        dma16(kpage + off, koff, lds_addr(&smem_k[stage][first]));
+        dma16(vpage + off, voff, lds_addr(&smem_v[stage][first]));
       }
       return valid;
     }
@@ -145,8 +154,8 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
       const int slot = first + lane, row = slot / P;
       const int pg = (int)fdiv(base + row, a.page), off = base + row - pg * (int)a.page.d;
       const int64_t page = pages.at(pg);
-      const char* kp = kbase + page * a.k_page + (off - lane / P) * (DIM * 2) + koff;
-      const char* vp = vbase + page * a.v_page + (off - lane / P) * (DIM * 2) + voff;
+      const char* kp = kbase + page * a.k_page + (int64_t)(off - lane / P) * ROW + koff;
+      const char* vp = vbase + page * a.v_page + (int64_t)(off - lane / P) * ROW + voff;
       if (!((valid >> row) & 1)) kp = vp = (const char*)&attn_zero;
       dma16(kp, lds_addr(&smem_k[stage][first]));
       dma16(vp, lds_addr(&smem_v[stage][first]));
@@ -282,10 +291,12 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
 #pragma unroll
       for (int x = 0; x < 16; ++x) o[d][x] = 0.0f;
   };
-  // Whether all of the wave's rows see all of the tile.
+  // Whether all of the wave's rows see all of the tile: those that start in
+  // [whole_lo, whole_hi], or before the sinks end.
+  const int whole_hi = wa - (KT - 1), whole_lo = a.window > 0 ? wb - a.window + 1 : 0;
+  const int whole_sinks = a.sinks - KT;
   auto whole = [&](int base, uint64_t valid) __attribute__((always_inline)) {
-    return base + KT - 1 <= wa && valid == ~0ull &&
-           !(a.window > 0 && base <= wb - a.window && base + KT > a.sinks);
+    return base <= whole_hi && valid == ~0ull && (base >= whole_lo || base <= whole_sinks);
   };
 
   // The fragment addresses move between the halves of the ring, so that within one
@@ -300,11 +311,13 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   auto walk = [&]() __attribute__((always_inline)) {
     clear();
     uint64_t valid[PAIR], next[PAIR];  // the keys of the tiles
+    int base[PAIR], nbase[PAIR];       // and where they start
     auto load = [&](int i, int half) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < PAIR; ++j) {
         next[j] = 0;
-        if (i + j < t1) next[j] = issue(i + j, half * PAIR + j);
+        nbase[j] = range.base(i + j);
+        if (i + j < t1) next[j] = issue(nbase[j], half * PAIR + j);
       }
     };
     load(t0, 0);
@@ -315,7 +328,10 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
 #pragma unroll 1
     for (int i = t0; i < t1; i += PAIR, half ^= 1) {
 #pragma unroll
-      for (int j = 0; j < PAIR; ++j) valid[j] = next[j];
+      for (int j = 0; j < PAIR; ++j) {
+        valid[j] = next[j];
+        base[j] = nbase[j];
+      }
       // these tiles have landed for every wave, and every wave is done with the last
       dma_wait<0>();
       lds_wait();
@@ -324,11 +340,10 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
 #pragma unroll
       for (int j = 0; j < PAIR; ++j) {
         if (i + j >= t1) break;
-        const int base = range.base(i + j);
         __builtin_amdgcn_s_setprio(1);
         scores(j);
         __builtin_amdgcn_s_setprio(0);
-        if (!whole(base, valid[j])) hide(base, valid[j]);
+        if (!whole(base[j], valid[j])) hide(base[j], valid[j]);
         softmax();
         __builtin_amdgcn_s_setprio(1);
         values(j);
@@ -345,7 +360,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
     for (int i = t0; i < t1; ++i) {
       __syncthreads();
       const int base = range.base(i);
-      const uint64_t valid = issue(i, 0);
+      const uint64_t valid = issue(base, 0);
       dma_wait<0>();
       __syncthreads();
       scores(0);
