@@ -136,31 +136,43 @@ template <typename E> __device__ __forceinline__ uint32_t nonfinite16(uint4 u) {
 // so the grid needs no host knowledge of the lengths; tiles past a request's
 // last row are empty.
 struct RowTile {
-  int req, start, len;  // request, its first token row and token count
-  int first, rows;      // first row of the tile, rows of the request
+  int req, start, len, seq;  // request, its first token row, token count and length
+  int first, rows;           // first row of the tile, rows of the request
 };
 template <int ROWS>
 __device__ __forceinline__ RowTile find_tile(const AttnLaunch& a, int tile, int lane) {
-  int lo = 0, hi = a.n;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 63) / 64;
-    const int i = lo + lane * step;
-    bool in = lane == 0;
-    if (!in && i < hi) {
-      const int c = min(max(a.cu[i], 0), a.total);
-      in = c * a.group / ROWS + i <= tile;
-    }
-    const int k = __popcll(__ballot(in)) - 1;
-    lo += k * step;
-    hi = min(hi, lo + step);
-  }
   RowTile t;
-  t.req = lo;
-  t.start = min(max(a.cu[lo], 0), a.total);
-  const int end = min(max(a.cu[lo + 1], t.start), a.total);
-  t.len = end - t.start;
+  if (a.n < 64) {
+    // one round trip: lane i reads request i
+    const int i = min(lane, a.n - 1);
+    const int c = min(max(a.cu[i], 0), a.total);
+    const int last = min(max(a.cu[a.n], 0), a.total), seq = a.seq[i];
+    t.req = __popcll(__ballot(lane == 0 || (lane < a.n && c * a.group / ROWS + lane <= tile))) - 1;
+    t.start = __builtin_amdgcn_readlane(c, t.req);
+    const int end = t.req + 1 < a.n ? __builtin_amdgcn_readlane(c, t.req + 1) : last;
+    t.len = max(end, t.start) - t.start;
+    t.seq = max(__builtin_amdgcn_readlane(seq, t.req), 0);
+  } else {
+    int lo = 0, hi = a.n;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 63) / 64;
+      const int i = lo + lane * step;
+      bool in = lane == 0;
+      if (!in && i < hi) {
+        const int c = min(max(a.cu[i], 0), a.total);
+        in = c * a.group / ROWS + i <= tile;
+      }
+      const int k = __popcll(__ballot(in)) - 1;
+      lo += k * step;
+      hi = min(hi, lo + step);
+    }
+    t.req = lo;
+    t.start = min(max(a.cu[lo], 0), a.total);
+    t.len = min(max(a.cu[lo + 1], t.start), a.total) - t.start;
+    t.seq = max(a.seq[lo], 0);
+  }
   t.rows = t.len * a.group;
-  t.first = (tile - (t.start * a.group / ROWS + lo)) * ROWS;
+  t.first = (tile - (t.start * a.group / ROWS + t.req)) * ROWS;
   return t;
 }
 
@@ -170,6 +182,7 @@ __device__ __forceinline__ RowTile request_tile(const AttnLaunch& a, int req) {
   t.req = req;
   t.start = min(max(a.cu[req], 0), a.total);
   t.len = min(max(a.cu[req + 1], t.start), a.total) - t.start;
+  t.seq = max(a.seq[req], 0);
   t.rows = t.len * a.group;
   t.first = 0;
   return t;

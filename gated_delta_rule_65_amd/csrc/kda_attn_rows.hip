@@ -66,8 +66,7 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(const AttnLaunch a) {
   const RowTile rt = BY_REQUEST ? request_tile(a, blockIdx.x / a.hkv)
                                 : find_tile<16 * RB>(a, blockIdx.x / a.hkv, lane);
   if (rt.rows > a.rows_limit) return;
-  const int seq = max(a.seq[rt.req], 0);
-  const int pos0 = seq - rt.len;
+  const int seq = rt.seq, pos0 = seq - rt.len;
   const float c = a.scale * LOG2E;
   constexpr float BIAS = [] {
     if constexpr (R::F32) return 0.0f;

@@ -56,8 +56,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   const RowTile rt = find_tile<32 * NW>(a, (int)(work / a.hkv), lane);
   if (rt.first >= rt.rows || rt.rows <= a.rows_limit) return;
   const int rows = min(32 * NW, rt.rows - rt.first);
-  const int seq = max(a.seq[rt.req], 0);
-  const int pos0 = seq - rt.len;
+  const int seq = rt.seq, pos0 = seq - rt.len;
   const KeyRange<KT> range(a, pos0 + (int)fdiv(rt.first, a.gdiv),
                            pos0 + (int)fdiv(rt.first + rows - 1, a.gdiv), seq);
   int per;

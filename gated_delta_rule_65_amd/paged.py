@@ -331,13 +331,16 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, scal
     the request's first `sinks` ones.  A row that sees no key gets zeros; rows behind
     cu_seqlens[n] are left as they are (undefined where the output is allocated here).
 
-    max_new_len: the longest request's new tokens, a planning hint (1 for decode).
+    max_new_len: the longest request's new tokens, a planning hint (1 for decode; taken
+    from cu_seqlens when that is a host tensor); results do not depend on it.
     splits: 0 lets the library cut long key ranges; else at most that many pieces.
     workspace: optional scratch of paged_attention_workspace_bytes(), for one call at
     a time.  Returns out [T, Hq, D], or (out, lse [T, Hq] fp32) with return_lse."""
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         _fail("cu_seqlens must be [n + 1]")
     n = cu_seqlens.shape[0] - 1
+    if max_new_len is None and n > 0 and cu_seqlens.device.type == "cpu":
+        max_new_len = max(0, int((cu_seqlens[1:] - cu_seqlens[:-1]).max()))
     a = _attention_args(q, k_cache, v_cache, block_table, n, scale, window, sinks, max_new_len,
                         splits)
     dev = q.device

@@ -124,7 +124,7 @@ kda_status kda_kv_append(const kda_kv_append_args *a);
  * Scores, softmax statistics and sums are held in fp32; for 16-bit types the
  * probabilities are rounded to the input type for their product with V, and out
  * is rounded once.  A row that sees no key (a position below 0, no page) gets
- * zeros and lse = -inf.  What lies at positions that a row does not see does not
+ * zeros and lse = -inf, as does one whose scores are all -inf.  What lies at positions that a row does not see does not
  * reach it, be it infinite or NaN.  Rows of out and lse behind the last request
  * are left as they are.  A length beyond the table's width reads the table's
  * positions only.

@@ -49,10 +49,10 @@ def make(ctx, new, hq, hkv, dim, page, dtype, seed=0, pad_rows=0, extra_cols=2, 
         at += used[i]
         k = (scale_k * torch.randn(total[i], hkv, dim, generator=g)).to(dtype)
         v = torch.randn(total[i], hkv, dim, generator=g).to(dtype)
-        for j in range(total[i]):
-            pg = int(table[i, j // page])
-            kc[pg, :, j % page] = k[j]
-            vc[pg, :, j % page] = v[j]
+        j = torch.arange(total[i])
+        pg = table[i, j // page].long()
+        kc[pg, :, j % page] = k
+        vc[pg, :, j % page] = v
         keys.append(k)
         values.append(v)
     for i, p in holes:
@@ -62,8 +62,8 @@ def make(ctx, new, hq, hkv, dim, page, dtype, seed=0, pad_rows=0, extra_cols=2, 
     return Case(q, kc, vc, table, cu, torch.tensor(total, dtype=torch.int32), keys, values)
 
 
-def attention(c, page, scale, window=0, sinks=0):
-    """(out, lse, tol_out, tol_lse) in 64 bits.  The tolerances follow the rounding
+def attention(c, page, scale, window=0, sinks=0, rows=None):
+    """(out, lse, tol_out, tol_lse) in 64 bits, of all rows or of the listed ones.  The tolerances follow the rounding
     steps of an fp32 softmax: a score is a dot product of D terms, its exponent
     a difference of numbers up to X; every weight is off by at most the relative
     w below, the probabilities are rounded to the input type (half a step each)
@@ -83,6 +83,8 @@ def attention(c, page, scale, window=0, sinks=0):
         j = np.arange(L)
         paged = np.array([int(c.table[i, x // page]) >= 0 for x in range(L)], dtype=bool)
         for x in range(a, b):
+            if rows is not None and x not in rows:
+                continue
             p = L - (b - a) + (x - a)
             see = (j <= p) & paged
             if window:
@@ -103,7 +105,10 @@ def attention(c, page, scale, window=0, sinks=0):
                     rel = 2.0 ** -24 * (2 * (dim + 4) * dots + 6 * np.abs(s).max() + idx.size + 16)
                     A = w @ np.abs(vv)
                 p_round = 0.0 if dtype == torch.float32 else half
-                tiny = idx.size * 2.0 ** -31 * np.abs(vv).max() + 2.0 ** -24 if dtype == torch.float16 else 0.0
+                # fp16 leaves its normal range below 2^-14: the probabilities (scaled by 2^6)
+                # and the output are then off by half of its smallest step, 2^-25
+                most = np.abs(vv[np.isfinite(vv)]).max(initial=0.0)
+                tiny = idx.size * 2.0 ** -31 * most + 2.0 ** -25 if dtype == torch.float16 else 0.0
                 tol[x, h] = A * (p_round + 2 * rel) + half * np.abs(out[x, h]) + tiny
                 tol_lse[x, h] = 2 * rel + 2.0 ** -22 * (abs(lse[x, h]) + 1)
     return out, lse, tol, tol_lse

@@ -177,6 +177,101 @@ def test_equal_calls_give_equal_bits():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+# Calls whose rows fill the chip with 256-row tiles over a wide table take those; the
+# others above take 128-row tiles.  (ctx, new, heads, dim, page, dtype, window, sinks)
+WIDE = {
+    "one_request": ([3], [1100], 64, 64, 128, 16, BF, 0, 0),
+    "ragged_grouped": ([700, 0, 5, 130], [900, 129, 1, 1070], 32, 8, 128, 64, HF, 0, 0),
+    "window_64_dim": ([33500, 0], [700, 600], 64, 16, 64, 48, BF, 33000, 6),
+}
+
+
+def wide_case(name):
+    ctx, new, hq, hkv, dim, page, dt, window, sinks = WIDE[name]
+    c = R.make(ctx, new, hq, hkv, dim, page, dt, seed=17, pad_rows=2)
+    table = torch.full((len(ctx), 65536 // page), -1, dtype=torch.int32)
+    table[:, :c.table.shape[1]] = c.table
+    c.table = table
+    return c, page, window, sinks
+
+
+def check_rows(c, page, got, window, sinks, count=8):
+    """The first and last rows of every request, and some between."""
+    out, lse = got
+    g = torch.Generator().manual_seed(3)
+    T = int(c.cu[-1])
+    rows = set(torch.randint(0, T, (count,), generator=g).tolist())
+    rows |= {int(x) for x in c.cu[:-1]} | {int(x) - 1 for x in c.cu[1:]}
+    ref, rl, tol, tl = R.attention(c, page, c.q.shape[-1] ** -0.5, window, sinks, rows=rows)
+    r = sorted(rows)
+    with np.errstate(all="ignore"):
+        o, l = out.double().numpy()[r], lse.double().numpy()[r]
+        fine = np.isfinite(ref[r])
+        assert np.array_equal(np.isfinite(o), fine) and np.array_equal(np.isnan(o), np.isnan(ref[r]))
+        assert np.all(np.abs(o - ref[r])[fine] <= tol[r][fine])
+        fine = np.isfinite(rl[r])
+        assert np.all(np.abs(l - rl[r])[fine] <= tl[r][fine])
+    assert torch.all(out[T:] == 7) and torch.all(lse[T:] == 7)
+
+
+@pytest.mark.parametrize("name", list(WIDE))
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_wide_tiles_match_64_bits(name, splits):
+    c, page, window, sinks = wide_case(name)
+    check_rows(c, page, attend(c, page, window, sinks, splits=splits), window, sinks)
+
+
+@pytest.mark.parametrize("name", list(WIDE))
+def test_wide_tiles_keep_hidden_values_out(name):
+    c, page, window, sinks = wide_case(name)
+    for i in range(len(c.keys)):
+        L = int(c.seq[i])
+        for pos, what in ((L - 1, float("nan")), (L // 2, float("inf"))):
+            c.values[i][pos, 0, 3] = what
+            c.v_cache[int(c.table[i, pos // page]), 0, pos % page, 3] = what
+    check_rows(c, page, attend(c, page, window, sinks), window, sinks)
+
+
+def small_reference(q, k, v, pos, key_pos, window, sinks, scale):
+    """One row's output from its visible keys, in 64 bits."""
+    see = (key_pos <= pos) & ((pos - key_pos < window) | (key_pos < sinks))
+    s = scale * (k[see].double() @ q.double())
+    return torch.softmax(s, 0) @ v[see].double()
+
+
+@pytest.mark.parametrize("new", [1, 80])
+@pytest.mark.parametrize("page,pages,table_at", [
+    (16, 1 << 21, 1 << 21),        # pages past 2^32 bytes of the pool
+    (1 << 25, 2, 1),               # one page of 2^32 bytes
+])
+def test_offsets_past_32_bits(page, pages, table_at, new):
+    """A pool of 2^25 tokens and more per head, of which the call reads the end."""
+    dim, window, sinks = 64, 70, 3
+    L = page * pages // 2 if page > 16 else 4000
+    g = torch.Generator(device=DEV).manual_seed(1)
+    print("offsets", page, pages, new, flush=True)
+    kc = torch.empty(pages, 1, page, dim, dtype=BF, device=DEV)
+    vc = torch.empty(pages, 1, page, dim, dtype=BF, device=DEV)
+    cols = -(-L // page)
+    table = (table_at - 1 - torch.arange(cols, device=DEV)).to(torch.int32)[None]
+    key_pos = torch.cat([torch.arange(sinks, device=DEV), torch.arange(L - new - window, L, device=DEV)])
+    slots = table[0, key_pos // page].long() * page + key_pos % page
+    k, v = (torch.randn(key_pos.numel(), 1, dim, device=DEV, generator=g).to(BF) for _ in range(2))
+    paged.kv_append(k, v, kc, vc, slots)
+    assert torch.equal(kc.view(-1, dim)[slots], k[:, 0]) and torch.equal(vc.view(-1, dim)[slots], v[:, 0])
+    q = torch.randn(new, 1, dim, device=DEV, generator=g).to(BF)
+    out = paged.paged_attention(q, kc, vc, table, torch.tensor([0, new], device=DEV),
+                                torch.tensor([L], device=DEV), window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    for x in range(new):
+        ref = small_reference(q[x, 0], k[:, 0], v[:, 0], L - new + x, key_pos, window, sinks, dim ** -0.5)
+        # a probability and the output are each rounded by at most 2^-8 of their size,
+        # and the weights sum to one: 2^-8 (max |v| + |ref|), with a part in a hundred
+        # for the fp32 steps
+        tol = 1.01 * 2.0 ** -8 * (v.double().abs().max() + ref.abs())
+        assert torch.all((out[x, 0].double() - ref).abs() <= tol), x
+
+
 # ------------------------------------------------------------- tables, append
 
 TABLES = {
