@@ -171,9 +171,15 @@ class HipEvents:
 
 # ------------------------------------------------------------------- helpers
 
+# The paged attention sources, which none of these workloads runs.
+NOT_KDA = ("kda_attn", "kda_page_tables", "kda_paged")
+
+
 def source_hash():
     h = hashlib.sha256()
     for p in sorted(glob.glob(os.path.join(ROOT, "gated_delta_rule_65_amd", "csrc", "*"))):
+        if os.path.basename(p).startswith(NOT_KDA):
+            continue
         with open(p, "rb") as f:
             h.update(os.path.basename(p).encode())
             h.update(f.read())

@@ -62,9 +62,9 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(const AttnLaunch a) {
   const int lane = threadIdx.x & 63, wave = wave_of();
   const int l16 = lane & 15, gq = lane >> 4;
   // heads fastest, so that neighbouring workgroups (and one XCD's) share pages
-  const int kvh = blockIdx.x % a.hkv, split = blockIdx.y;
-  const RowTile rt = BY_REQUEST ? request_tile(a, blockIdx.x / a.hkv)
-                                : find_tile<16 * RB>(a, blockIdx.x / a.hkv, lane);
+  const uint32_t unit = fdiv(blockIdx.x, a.hdiv);
+  const int kvh = (int)(blockIdx.x - unit * a.hkv), split = blockIdx.y;
+  const RowTile rt = BY_REQUEST ? request_tile(a, (int)unit) : find_tile<16 * RB>(a, (int)unit, lane);
   if (rt.rows > a.rows_limit) return;
   const int seq = rt.seq, pos0 = seq - rt.len;
   const float c = a.scale * LOG2E;

@@ -51,9 +51,9 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   const int lane = threadIdx.x & 63, wave = wave_of();
   const int l32 = lane & 31, h = lane >> 5;
   // later tiles have more keys: they go first
-  const int64_t work = (int64_t)gridDim.x - 1 - blockIdx.x;
-  const int kvh = (int)(work % a.hkv), split = blockIdx.y;
-  const RowTile rt = find_tile<32 * NW>(a, (int)(work / a.hkv), lane);
+  const uint32_t work = gridDim.x - 1 - blockIdx.x, unit = fdiv(work, a.hdiv);
+  const int kvh = (int)(work - unit * a.hkv), split = blockIdx.y;
+  const RowTile rt = find_tile<32 * NW>(a, (int)unit, lane);
   if (rt.first >= rt.rows || rt.rows <= a.rows_limit) return;
   const int rows = min(32 * NW, rt.rows - rt.first);
   const int seq = rt.seq, pos0 = seq - rt.len;

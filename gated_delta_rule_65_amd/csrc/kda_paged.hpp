@@ -68,7 +68,7 @@ struct AttnLaunch {
   int64_t table_stride;
   int dtype, n, total, hq, hkv, group, dim, num_pages, max_pages;
   int64_t key_capacity;    // max_pages * page size
-  FastDiv page, gdiv;
+  FastDiv page, gdiv, hdiv;  // by the page size, the group, hkv
   int window, sinks;       // window 0: every earlier key
   float scale;
   int row_blocks;          // rows kernel: 16-row blocks per wave (1 or 2)

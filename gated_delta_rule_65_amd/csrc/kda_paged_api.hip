@@ -113,6 +113,7 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
   L.key_capacity = (int64_t)a->max_pages * a->page_size;
   L.page = kda::fast_div((uint32_t)a->page_size);
   L.gdiv = kda::fast_div((uint32_t)L.group);
+  L.hdiv = kda::fast_div((uint32_t)L.hkv);
   // positions stay below 2^30, so larger windows and sink counts change nothing
   L.window = a->window < MAX_KEYS ? a->window : (int)MAX_KEYS;
   L.sinks = a->sinks < MAX_KEYS ? a->sinks : (int)MAX_KEYS;

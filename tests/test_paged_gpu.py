@@ -171,6 +171,34 @@ def test_hint_and_splits_change_sums_only():
             check(c, 16, attend(c, 16, max_new_len=hint, splits=splits))
 
 
+def test_many_requests_and_heads_that_are_no_power_of_two():
+    """More requests than one look at the offsets covers, in both kernels."""
+    ctx = [(37 * i) % 60 for i in range(150)]
+    for new, hq, hkv, dt in (([1] * 150, 9, 3, BF), ([(i * 7) % 4 for i in range(150)], 6, 3, FP),
+                             ([(i * 5) % 19 for i in range(150)], 21, 7, HF)):
+        c = R.make(ctx, new, hq, hkv, 64, 16, dt, seed=11, pad_rows=1)
+        check(c, 16, attend(c, 16, max_new_len=max(new)))
+
+
+def test_calls_without_tokens_requests_or_pages():
+    c = R.make([5], [2], 4, 2, 64, 16, BF)
+    q, kc, vc = c.q.to(DEV), c.k_cache.to(DEV), c.v_cache.to(DEV)
+    none = torch.zeros(0, 3, dtype=torch.int32, device=DEV)
+    out = torch.full_like(q, 7.0)
+    paged.paged_attention(q, kc, vc, none, torch.zeros(1, dtype=torch.int32, device=DEV),
+                          torch.zeros(0, dtype=torch.int32, device=DEV), output=out)
+    assert torch.all(out == 7)
+    empty = paged.paged_attention(q[:0], kc, vc, c.table.to(DEV), torch.tensor([0, 0], device=DEV),
+                                  c.seq.to(DEV))
+    assert empty.shape == (0, 4, 64)
+    out, lse = paged.paged_attention(q, kc, vc, torch.zeros(1, 0, dtype=torch.int32, device=DEV),
+                                     c.cu.to(DEV), c.seq.to(DEV), return_lse=True)
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+    out, lse = paged.paged_attention(q, kc, vc, c.table.to(DEV), c.cu.to(DEV),
+                                     torch.zeros(1, dtype=torch.int32, device=DEV), return_lse=True)
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+
+
 def test_equal_calls_give_equal_bits():
     c = R.make([900, 31], [60, 1], 8, 2, 128, 16, BF, seed=6)
     a, b = attend(c, 16), attend(c, 16)
