@@ -1,5 +1,5 @@
-// Paged attention of few rows per request (decode, short drafts; every fp32
-// call), and the join of split partials.
+// Paged attention of few rows per request (decode, short drafts) and of every fp32
+// call, and the join of split partials.
 //
 // out = softmax(scale q K^T) V over a request's visible keys, in one pass with
 // the running maximum m and sum l of the softmax (exponents in base 2, the scale
@@ -65,7 +65,6 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(const AttnLaunch a) {
   const uint32_t unit = fdiv(blockIdx.x, a.hdiv);
   const int kvh = (int)(blockIdx.x - unit * a.hkv), split = blockIdx.y;
   const RowTile rt = BY_REQUEST ? request_tile(a, (int)unit) : find_tile<16 * RB>(a, (int)unit, lane);
-  if (rt.rows > a.rows_limit) return;
   const int seq = rt.seq, pos0 = seq - rt.len;
   const float c = a.scale * LOG2E;
   constexpr float BIAS = [] {
@@ -98,7 +97,7 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(const AttnLaunch a) {
     const int pb = pos0 + (int)fdiv(first + rows - 1, a.gdiv);
     const KeyRange<KT> range(a, pa, pb, seq);
     int per;
-    const int splits = split_of(range.tiles, a.rows_splits, a.rows_min_keys / KT, per);
+    const int splits = split_of(range.tiles, a.splits, a.min_keys / KT, per);
     if (split >= splits) continue;
     const int t0 = split * per, nt = max(0, min(per, range.tiles - t0));
 
@@ -518,12 +517,12 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnLaunch a, int split
 template <typename E, int DIM, int RB> hipError_t rows_go(const AttnLaunch& L) {
   if (L.by_request) {
     hipLaunchKernelGGL((rows_kernel<E, DIM, RB, true>),
-                       dim3((unsigned)(L.n * L.hkv), (unsigned)L.rows_splits), dim3(64 * WAVES), 0,
+                       dim3((unsigned)(L.n * L.hkv), (unsigned)L.splits), dim3(64 * WAVES), 0,
                        (hipStream_t)L.stream, L);
   } else {
     const int64_t tiles = (int64_t)L.total * L.group / (16 * RB) + L.n;
     hipLaunchKernelGGL((rows_kernel<E, DIM, RB, false>),
-                       dim3((unsigned)(tiles * L.hkv), (unsigned)L.rows_splits), dim3(64 * WAVES), 0,
+                       dim3((unsigned)(tiles * L.hkv), (unsigned)L.splits), dim3(64 * WAVES), 0,
                        (hipStream_t)L.stream, L);
   }
   return hipGetLastError();
@@ -536,16 +535,15 @@ template <typename E> hipError_t rows_dim(const AttnLaunch& L) {
 }
 
 // Four waves share a row where there are many splits of few rows; with many rows,
-// most of which were not split, a wave looks at several of them: 16 where only the
-// rows kernel cuts (its rows are few), 4 where the tiles kernel does.
+// some of which were not split, a wave looks at four of them.
 template <typename E, int DIM> hipError_t join_go(const AttnLaunch& L) {
-  const int splits = L.rows_splits > L.tile_splits ? L.rows_splits : L.tile_splits;
+  const int splits = L.splits;
   const int64_t rows = (int64_t)L.total * L.hq;
   if (splits > 8 && rows <= 8192) {
     hipLaunchKernelGGL((join_kernel<E, DIM, 4>), dim3((unsigned)rows), dim3(256), 0,
                        (hipStream_t)L.stream, L, splits, 1);
   } else {
-    const int each = rows <= 16384 ? 1 : L.tile_splits > 1 ? 4 : 16;
+    const int each = rows <= 16384 ? 1 : 4;
     hipLaunchKernelGGL((join_kernel<E, DIM, 1>), dim3((unsigned)((rows + 4 * each - 1) / (4 * each))),
                        dim3(256), 0, (hipStream_t)L.stream, L, splits, each);
   }

@@ -54,13 +54,13 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   const uint32_t work = gridDim.x - 1 - blockIdx.x, unit = fdiv(work, a.hdiv);
   const int kvh = (int)(work - unit * a.hkv), split = blockIdx.y;
   const RowTile rt = find_tile<32 * NW>(a, (int)unit, lane);
-  if (rt.first >= rt.rows || rt.rows <= a.rows_limit) return;
+  if (rt.first >= rt.rows) return;
   const int rows = min(32 * NW, rt.rows - rt.first);
   const int seq = rt.seq, pos0 = seq - rt.len;
   const KeyRange<KT> range(a, pos0 + (int)fdiv(rt.first, a.gdiv),
                            pos0 + (int)fdiv(rt.first + rows - 1, a.gdiv), seq);
   int per;
-  const int splits = split_of(range.tiles, a.tile_splits, a.tile_min_keys / KT, per);
+  const int splits = split_of(range.tiles, a.splits, a.min_keys / KT, per);
   if (split >= splits) return;
   const int t0 = split * per, t1 = min(range.tiles, t0 + per);
 
@@ -306,8 +306,10 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
 #pragma unroll
     for (int d = 0; d < DV; ++d) va[d] += by;
   };
-  // PAIR tiles between barriers, while the DMA fills the other half of the ring.
-  auto walk = [&]() __attribute__((always_inline)) {
+  // PAIR tiles between barriers, while the DMA fills the other half of the ring.  A
+  // wave without rows (in a request's last tile) does its part of the loads only.
+  auto walk = [&](auto busy) __attribute__((always_inline)) {
+    constexpr bool BUSY = decltype(busy)::value;
     clear();
     uint64_t valid[PAIR], next[PAIR];  // the keys of the tiles
     int base[PAIR], nbase[PAIR];       // and where they start
@@ -336,6 +338,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
       lds_wait();
       __builtin_amdgcn_s_barrier();
       load(i + PAIR, half ^ 1);
+      if constexpr (!BUSY) continue;
 #pragma unroll
       for (int j = 0; j < PAIR; ++j) {
         if (i + j >= t1) break;
@@ -350,7 +353,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
       }
       turn(half ? -PAIR * STAGE : PAIR * STAGE);
     }
-    if (half) turn(-PAIR * STAGE);
+    if (BUSY && half) turn(-PAIR * STAGE);
   };
   // The same tile by tile, with the hidden keys' values kept out of the sums.
   auto walk_carefully = [&]() __attribute__((always_inline)) {
@@ -369,7 +372,8 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
       else values_by_key(base, 0, valid);
     }
   };
-  walk();
+  if (32 * wave < rows) walk(std::true_type{});
+  else walk(std::false_type{});
   // a hidden infinity or NaN of V has spoilt the sums of its tile: once more, carefully
   float z = 0.0f;  // becomes NaN if any sum is not finite
 #pragma unroll
@@ -407,7 +411,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
 
 template <typename E, int DIM, int NW> hipError_t tiles_go(const AttnLaunch& L) {
   const int64_t tiles = (int64_t)L.total * L.group / (32 * NW) + L.n;
-  hipLaunchKernelGGL((tiles_kernel<E, DIM, NW>), dim3((unsigned)(tiles * L.hkv), (unsigned)L.tile_splits),
+  hipLaunchKernelGGL((tiles_kernel<E, DIM, NW>), dim3((unsigned)(tiles * L.hkv), (unsigned)L.splits),
                      dim3(64 * NW), 0, (hipStream_t)L.stream, L);
   return hipGetLastError();
 }

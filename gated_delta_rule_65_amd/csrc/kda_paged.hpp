@@ -71,12 +71,10 @@ struct AttnLaunch {
   FastDiv page, gdiv, hdiv;  // by the page size, the group, hkv
   int window, sinks;       // window 0: every earlier key
   float scale;
+  int tile_waves;          // tiles kernel: waves of 32 rows (4 or 8); 0: the rows kernel runs
   int row_blocks;          // rows kernel: 16-row blocks per wave (1 or 2)
-  int rows_limit;          // rows kernel: a request with more rows is the tiles kernel's
   int by_request;          // rows kernel: a workgroup per request, not per row tile
-  int rows_splits, tile_splits;
-  int rows_min_keys, tile_min_keys;  // keys per split at least
-  int tile_waves;          // tiles kernel: waves of 32 rows, 0 = not launched
+  int splits, min_keys;    // splits of a visit at most, and keys of one at least
   void* stream;
 };
 hipError_t launch_attn_rows(const AttnLaunch& L);

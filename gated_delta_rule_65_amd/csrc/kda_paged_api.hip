@@ -125,45 +125,41 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
   int64_t keys = L.key_capacity;
   if (L.window > 0 && (int64_t)L.window + L.sinks + most_new < keys)
     keys = (int64_t)L.window + L.sinks + most_new;
-  // Requests of up to 32 rows per kv head, and every fp32 one, are the rows kernel's;
-  // a request with more fills the matrix tiles.
+  // The rows kernel serves calls whose requests have up to 32 rows per kv head, and
+  // fp32; else all requests go through the matrix tiles, the short ones beside the
+  // chunks in one launch (33 mixed requests: 86 us against 101 us in a launch each).
   const int64_t most_rows = most_new * L.group, rows = a->total_tokens * a->hq;
+  const int64_t group_rows = a->total_tokens * L.group;
   const bool tiles = a->dtype != KDA_F32 && most_rows > 32;
-  const bool few = !tiles || a->n > 1;
   L.row_blocks = most_rows > 16 ? 2 : 1;
-  L.rows_limit = !tiles ? INT32_MAX : few ? 32 : 0;
-  L.by_request = most_rows <= 32 || tiles;
+  L.by_request = most_rows <= 32;
   // Eight waves (256 rows) a workgroup where key ranges are long and the rows fill the
   // chip with them, else four: kda_attn_tiles.hip says why, with both sides measured.
-  const int64_t tile_rows = a->total_tokens * L.group;
-  L.tile_waves = !tiles ? 0 : keys >= 32768 && ceil_div(tile_rows, 256) * a->hkv >= 256 ? 8 : 4;
-  const int64_t cap = rows > 0 ? (int64_t)(MAX_PARTIALS / ((size_t)rows * a->head_dim * 4)) : 1;
+  L.tile_waves = !tiles ? 0 : keys >= 32768 && ceil_div(group_rows, 256) * a->hkv >= 256 ? 8 : 4;
   // Splits: pieces of long visits small enough to even out ragged lengths and to give
-  // every compute unit work, in a grid of about `grid` workgroups, so that the many
-  // requests that are not split do not swell it.
-  auto splits_of = [&](int64_t base, int64_t least, int64_t grid) {
-    int64_t want = a->splits > 0 ? a->splits : base > 0 ? grid / base : 1;
-    if (want > MAX_SPLITS) want = MAX_SPLITS;
-    if (want > keys / least) want = keys / least;
-    if (want > cap) want = cap;
-    return want > 1 ? (int)want : 1;
-  };
-  const int64_t units = L.by_request ? (int64_t)a->n * a->hkv
-                                     : ceil_div(a->total_tokens * L.group, 16 * L.row_blocks) * a->hkv;
-  L.rows_min_keys = units >= 1024 ? 2048 : units >= 256 ? 1024 : 256;
-  L.rows_splits = few ? splits_of(units, L.rows_min_keys, L.by_request ? 16384 : 2048) : 1;
-  // A split row costs the tiles kernel its fp32 partials, so they are cut only where
-  // there are few of them for the chip, counting ragged requests as fewer.
-  const int64_t tile_units = tiles ? ceil_div(tile_rows, 32 * L.tile_waves) * a->hkv : 0;
-  const int64_t enough = (L.tile_waves == 8 ? 256 : 512) * (a->n > 1 ? 3 : 1);
-  L.tile_min_keys = tile_units >= 256 ? 1024 : 512;
-  L.tile_splits = tiles && (a->splits > 0 || tile_units < enough)
-                      ? splits_of(tile_units, L.tile_min_keys, tile_units >= 256 ? 8192 : 1024) : 1;
-  const int most = L.rows_splits > L.tile_splits ? L.rows_splits : L.tile_splits;
+  // every compute unit work, in a grid that the many requests that are not split do not
+  // swell.  A split row costs the tiles kernel its fp32 partials, so its rows are cut
+  // only where they are few for the chip, ragged requests counting a third.
+  int64_t units, grid;
+  if (tiles) {
+    units = ceil_div(group_rows, 32 * L.tile_waves) * a->hkv;
+    L.min_keys = units >= 256 ? 1024 : 512;
+    grid = units >= (L.tile_waves == 8 ? 256 : 512) * (a->n > 1 ? 3 : 1) ? 0 : units >= 256 ? 8192 : 1024;
+  } else {
+    units = L.by_request ? (int64_t)a->n * a->hkv : ceil_div(group_rows, 16 * L.row_blocks) * a->hkv;
+    L.min_keys = units >= 1024 ? 2048 : units >= 256 ? 1024 : 256;
+    grid = L.by_request ? 16384 : 2048;
+  }
+  int64_t want = a->splits > 0 ? a->splits : units > 0 ? grid / units : 1;
+  if (want > MAX_SPLITS) want = MAX_SPLITS;
+  if (want > keys / L.min_keys) want = keys / L.min_keys;
+  const int64_t cap = rows > 0 ? (int64_t)(MAX_PARTIALS / ((size_t)rows * a->head_dim * 4)) : 1;
+  if (want > cap) want = cap;
+  L.splits = want > 1 ? (int)want : 1;
   p.o_bytes = p.lse_bytes = p.n_bytes = 0;
-  if (most > 1) {
-    p.o_bytes = (size_t)most * rows * a->head_dim * 4;
-    p.lse_bytes = ((size_t)most * rows * 4 + 15) / 16 * 16;
+  if (L.splits > 1) {
+    p.o_bytes = (size_t)L.splits * rows * a->head_dim * 4;
+    p.lse_bytes = ((size_t)L.splits * rows * 4 + 15) / 16 * 16;
     p.n_bytes = ((size_t)rows * 4 + 15) / 16 * 16;
   }
   need = p.o_bytes + p.lse_bytes + p.n_bytes;
@@ -288,9 +284,7 @@ KDA_API kda_status kda_paged_attention(const kda_paged_attention_args* a) {
     L.part_n = (int32_t*)(ws + p.o_bytes + p.lse_bytes);
   }
   L.stream = a->stream;
-  hipError_t e = hipSuccess;
-  if (L.tile_waves > 0) e = kda::launch_attn_tiles(L);
-  if (e == hipSuccess && L.rows_limit > 0) e = kda::launch_attn_rows(L);
+  hipError_t e = L.tile_waves > 0 ? kda::launch_attn_tiles(L) : kda::launch_attn_rows(L);
   if (e == hipSuccess && need > 0) e = kda::launch_attn_join(L);
   if (e != hipSuccess) FAIL(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
   return (kda_status)kda::set_ok();
