@@ -7,20 +7,26 @@
 // O^T, so a row's maximum and sum take one swap between the wave's halves.
 //
 // Bound by the matrix cores and the vector unit together: a tile of 64 keys costs a
-// wave 32 products (1024 cycles for 128 channels) and about 240 vector instructions
-// with 32 exponentials (about as much), and a SIMD holds two waves (246 registers).
-// So the two have to be out of step, one multiplying while the other weighs:
-//  - They drift apart by themselves where barriers are rare and products go first
-//    (s_setprio).  2048 tokens on 131072 keys, 32 heads: 3.93 ms (1.11 PFLOP/s; 4.31
-//    ms in step, 4.46 ms with the phases held apart by barriers, 4.60 ms with one
-//    tile's products woven into the last one's softmax).
-//  - Fragment reads stay three ahead of their products (left to the compiler, each
-//    product waits for its own read: 5.9 ms).
-// Both shapes below have two waves per SIMD and 128 KB of LDS per compute unit.  Eight
-// waves (256 rows, two tiles a barrier) read each key half as often, which long visits
-// need; two workgroups of four waves (128 rows, a tile a barrier) even out ragged
-// requests (33 requests of 1 .. 700 tokens: 157 us against 184 us; 2048 tokens on
-// 131072 keys: 4.54 ms against 3.93 ms).
+// wave 32 products (1024 cycles for 128 channels) and about 100 vector instructions
+// beside 32 exponentials (nearly as much), and a SIMD holds two waves (256 registers).
+// So the two have to be out of step, one multiplying while the other weighs.  They
+// drift apart by themselves where barriers are rare; products go first (s_setprio).
+// 2048 tokens on 131072 keys, 32 heads on 8, takes 3.7 ms (1.17 PFLOP/s, matrix cores
+// 56 % busy; a large library product reaches 1.23).  Measured on the way, same case:
+//   a barrier a tile, both waves in step                          4.26 ms
+//   the phases of the two waves held apart by barriers            4.46 ms
+//   a tile's products woven into the softmax of the one before    4.60 ms
+//   two tiles a barrier                                           4.06 ms
+//   the same, products first                                      3.93 ms
+//   the same, fragment addresses constant within a ring half      3.82 ms
+// Fragment reads stay three ahead of their products: left to the compiler each product
+// waits for its own read (5.87 ms, with the phases held apart).
+//
+// Both shapes have two waves per SIMD and 128 KB of LDS per compute unit.  Eight waves
+// (256 rows, two tiles a barrier) read each key half as often, which long visits need;
+// two workgroups of four waves (128 rows, a tile a barrier) even out ragged requests
+// (33 requests of 1 .. 700 tokens: 157 us against 184 us; 2048 tokens on 131072 keys:
+// 4.54 ms against 3.93 ms, both without splits).
 #include "kda_attn.hpp"
 
 namespace kda {
@@ -42,7 +48,7 @@ template <typename E, int DIM, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   typedef typename Half<E>::frag frag;
   constexpr int P = DIM / 8;            // 16-byte pieces per row
-  constexpr int NI = P / NW > 0 ? P / NW : 1;  // DMA instructions per wave and tile
+  constexpr int NI = P / NW;            // DMA instructions per wave and tile, K or V
   constexpr int QS = DIM / 16, DV = DIM / 32;
   constexpr int RING = NW / 2, PAIR = RING / 2;  // tiles in LDS, tiles per barrier
   static_assert(P % NW == 0, "a tile splits evenly over the waves");
@@ -210,7 +216,8 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
     }
     __builtin_amdgcn_sched_group_barrier(MFMA, AHEAD, 0);
   };
-  auto hide = [&](int base, uint64_t valid) __attribute__((always_inline)) {  // keys hidden from the row, or absent
+  // Takes out the keys that are hidden from the row, or absent.
+  auto hide = [&](int base, uint64_t valid) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const uint32_t see = seen(a, base + 32 * k, qpos, (uint32_t)(valid >> (32 * k))) >> (4 * h);

