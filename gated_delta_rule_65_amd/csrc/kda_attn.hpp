@@ -173,6 +173,7 @@ __device__ __forceinline__ RowTile find_tile(const AttnLaunch& a, int tile, int 
   }
   t.rows = t.len * a.group;
   t.first = (tile - (t.start * a.group / ROWS + t.req)) * ROWS;
+  if (t.first < 0) t.rows = 0;  // offsets that decrease: no rows rather than wrong ones
   return t;
 }
 

@@ -68,6 +68,7 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(const AttnLaunch a) {
   const uint32_t unit = fdiv(blockIdx.x, a.hdiv);
   const int kvh = (int)(blockIdx.x - unit * a.hkv), split = blockIdx.y;
   const RowTile rt = BY_REQUEST ? request_tile(a, (int)unit) : find_tile<16 * RB>(a, (int)unit, lane);
+  if (rt.rows == 0) return;
   const int seq = rt.seq, pos0 = seq - rt.len;
   const float c = a.scale * LOG2E;
   constexpr float BIAS = [] {

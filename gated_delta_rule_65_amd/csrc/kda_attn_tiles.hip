@@ -60,7 +60,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
   const uint32_t work = gridDim.x - 1 - blockIdx.x, unit = fdiv(work, a.hdiv);
   const int kvh = (int)(work - unit * a.hkv), split = blockIdx.y;
   const RowTile rt = find_tile<32 * NW>(a, (int)unit, lane);
-  if (rt.first >= rt.rows) return;
+  if (rt.first >= rt.rows || rt.rows == 0) return;
   const int rows = min(32 * NW, rt.rows - rt.first);
   const int seq = rt.seq, pos0 = seq - rt.len;
   const KeyRange<KT> range(a, pos0 + (int)fdiv(rt.first, a.gdiv),

@@ -143,7 +143,10 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
   int64_t units, grid;
   if (tiles) {
     units = ceil_div(group_rows, 32 * L.tile_waves) * a->hkv;
-    L.min_keys = units >= 256 ? 1024 : 512;
+    // pieces of 2048 keys where requests are many (255 decodes beside a chunk of 512
+    // tokens: 364 us, with 1024 keys 414 us), shorter ones where they are few (33 mixed
+    // requests: 93 us with 1024 keys, 108 us with 2048; 512 tokens alone: 59 and 80 us)
+    L.min_keys = units + (int64_t)a->n * a->hkv >= 2048 ? 2048 : units >= 256 ? 1024 : 512;
     grid = units >= (L.tile_waves == 8 ? 256 : 512) * (a->n > 1 ? 3 : 1) ? 0 : units >= 256 ? 8192 : 1024;
   } else {
     units = L.by_request ? (int64_t)a->n * a->hkv : ceil_div(group_rows, 16 * L.row_blocks) * a->hkv;

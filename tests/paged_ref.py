@@ -81,7 +81,8 @@ def attention(c, page, scale, window=0, sinks=0, rows=None):
         L = int(c.seq[i])
         k, v = c.keys[i].double().numpy(), c.values[i].double().numpy()
         j = np.arange(L)
-        paged = np.array([int(c.table[i, x // page]) >= 0 for x in range(L)], dtype=bool)
+        paged = np.array([x // page < c.table.shape[1] and int(c.table[i, x // page]) >= 0
+                          for x in range(L)], dtype=bool)
         for x in range(a, b):
             if rows is not None and x not in rows:
                 continue

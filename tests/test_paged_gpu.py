@@ -53,6 +53,7 @@ CASES = {
     "decode_mqa_wide_group": ([40, 333], [1, 1], 40, 1, 128, 16, BF, 0, 0),
     "decode_fp32": ([0, 31, 32, 257], [1] * 4, 6, 2, 128, 16, FP, 0, 0),
     "decode_fp32_64": ([77, 0], [1, 1], 5, 1, 64, 20, FP, 0, 0),
+    "decode_fp32_wide_group": ([40, 333], [1, 1], 40, 1, 128, 16, FP, 0, 0),
     "draft_tokens": ([10, 0, 255], [4, 3, 5], 8, 2, 128, 16, BF, 0, 0),
     "odd_page": ([100, 47, 48, 49], [1, 2, 1, 50], 6, 2, 64, 48, HF, 0, 0),
     "page_of_one": ([70], [3], 2, 1, 64, 1, BF, 0, 0),
@@ -136,6 +137,43 @@ def test_missing_pages_hold_no_key(dt, new):
     page = 16
     c = R.make([90, 0], [new, 5], 4, 2, 128, page, dt, seed=4, holes=[(0, 0), (0, 3), (1, 0)])
     check(c, page, attend(c, page))
+
+
+def test_positions_past_the_table_hold_no_key():
+    """A table too narrow for the request: the positions that it lists are read."""
+    for dt, new in ((BF, 1), (HF, 70), (FP, 5)):
+        c = R.make([100], [new], 4, 2, 64, 16, dt, seed=12)
+        c.table = c.table[:, :3].contiguous()
+        check(c, 16, attend(c, 16))
+
+
+@pytest.mark.parametrize("dt,new", [(BF, 1), (HF, 90), (FP, 9)])
+def test_key_and_value_pools_with_strides_of_their_own(dt, new):
+    """Dense K pages, V pages that lie apart."""
+    c = R.make([50], [new], 4, 2, 128, 20, dt, seed=13)
+    pages = c.v_cache.shape[0]
+    room = torch.full((pages, c.v_cache[0].numel() + 64), float("nan"), dtype=dt)
+    room[:, :-64] = c.v_cache.reshape(pages, -1)
+    v = room.to(DEV)[:, :-64].view(c.v_cache.shape)
+    assert not v.is_contiguous()
+    print("strides", dt, new, flush=True)
+    out, lse = paged.paged_attention(c.q.to(DEV), c.k_cache.to(DEV), v, c.table.to(DEV), c.cu.to(DEV),
+                                     c.seq.to(DEV), return_lse=True)
+    torch.cuda.synchronize()
+    check(c, 20, (out.cpu(), lse.cpu()))
+    # and the append into them, from rows of different strides
+    k_rows, v_rows = c.keys[0].to(DEV), c.values[0].to(DEV)
+    wide = torch.zeros(k_rows.shape[0], 5, 128, dtype=dt, device=DEV)
+    wide[:, 1:3] = k_rows
+    j = torch.arange(k_rows.shape[0])
+    slots = (c.table[0, j // 20].long() * 20 + j % 20).to(DEV)
+    kc, vr = torch.zeros_like(c.k_cache, device=DEV), torch.zeros_like(room, device=DEV)
+    vc = vr[:, :-64].view(c.v_cache.shape)
+    paged.kv_append(wide[:, 1:3], v_rows, kc, vc, slots)
+    pg, off = slots // 20, slots % 20
+    assert torch.equal(kc[pg, :, off], k_rows) and torch.equal(vc[pg, :, off], v_rows)
+    assert torch.all(vr[:, -64:] == 0)
+    assert int((kc != 0).any(-1).sum()) == 2 * k_rows.shape[0]
 
 
 def test_lengths_below_the_new_tokens_leave_rows_empty():
