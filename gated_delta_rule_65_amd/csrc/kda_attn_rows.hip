@@ -458,19 +458,88 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(const AttnLaunch a) {
   }
 }
 
-// out = sum_s 2^(lse_s - top) O_s / sum_s 2^(lse_s - top) over the splits of a row,
-// in their order.  W waves share a row's splits (many splits, few rows), or each
-// wave takes `each` consecutive rows of which only some were split.
-template <typename E, int DIM, int W>
-__global__ __launch_bounds__(256) void join_kernel(const AttnLaunch a, int splits, int each) {
+// The join of a row's splits, in their order:
+// out = sum_s 2^(lse_s - top) O_s / sum_s 2^(lse_s - top).
+// Lane s weighs split s (there are at most 64): the weight, and what the weights sum to.
+__device__ __forceinline__ float split_weight(float e, float& base, float& sum) {
+  float top = e;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  base = top == NEG_INF ? 0.0f : top;
+  const float f = exp2_fast(e - base);
+  sum = f;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  return f;
+}
+__device__ __forceinline__ float lane_value(float x, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane));
+}
+
+template <typename E, int DIM>
+__device__ __forceinline__ void join_store(const AttnLaunch& a, int64_t row, const float* acc, float base,
+                                           float sum, int lane) {
   constexpr int V = DIM / 64;
-  __shared__ float sm[W > 1 ? W : 1][DIM];
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  E* dst = (E*)a.out + row * DIM + V * lane;
+#pragma unroll
+  for (int i = 0; i < V; ++i) dst[i] = from_f32<E>(acc[i] * inv);
+  if (a.lse != nullptr && lane == 0)
+    a.lse[row] = sum == 0.0f ? NEG_INF : (base + __log2f(sum)) * LN2;
+}
+
+// Few rows: four waves share one, a quarter of the splits each.  Bound by latency, so
+// nothing waits for the number of splits but the sums: all loads go out at once.
+template <typename E, int DIM> __global__ __launch_bounds__(256) void join_few_kernel(const AttnLaunch a) {
+  constexpr int V = DIM / 64, AT_ONCE = 16;
+  __shared__ float sm[4][DIM];
   const int lane = threadIdx.x & 63, wave = wave_of();
+  const int64_t rows = (int64_t)a.total * a.hq, row = blockIdx.x;
+  const int cut = a.part_n[row], c0 = a.cu[0], c1 = a.cu[a.n];
+  float e = lane < a.splits ? a.part_lse[lane * rows + row] : NEG_INF;
+  const float* src = a.part_o + row * DIM + V * lane;
+  float x[AT_ONCE][V];
+#pragma unroll
+  for (int j = 0; j < AT_ONCE; ++j) {
+    const int s = min(16 * wave + j, a.splits - 1);
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[j][i] = src[s * rows * DIM + i];
+  }
+  // only rows of the batch that were split
+  const int64_t first = (int64_t)min(max(c0, 0), a.total) * a.hq;
+  const int64_t last = (int64_t)min(max(c1, 0), a.total) * a.hq;
+  if (row < first || row >= last || cut <= 1) return;
+  const int n = min(cut, a.splits);
+  if (lane >= n) e = NEG_INF;
+  float base, sum, acc[V] = {};
+  const float f = split_weight(e, base, sum);
+#pragma unroll
+  for (int j = 0; j < AT_ONCE; ++j) {
+    const int s = 16 * wave + j;
+    const float g = lane_value(f, s);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = s < n ? fmaf(g, x[j][i], acc[i]) : acc[i];
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) sm[wave][V * lane + i] = acc[i];
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int w = 1; w < 4; ++w)
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] += sm[w][V * lane + i];
+  join_store<E, DIM>(a, row, acc, base, sum, lane);
+}
+
+// Many rows, some of which were not split: a wave looks at `each` consecutive ones.
+template <typename E, int DIM>
+__global__ __launch_bounds__(256) void join_kernel(const AttnLaunch a, int each) {
+  constexpr int V = DIM / 64;
+  const int lane = threadIdx.x & 63;
   const int64_t rows = (int64_t)a.total * a.hq;
-  // only the rows of the batch have partials
   const int64_t first = (int64_t)min(max(a.cu[0], 0), a.total) * a.hq;
   const int64_t last = (int64_t)min(max(a.cu[a.n], 0), a.total) * a.hq;
-  const int64_t r0 = W > 1 ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x * 4 + wave) * each;
+  const int64_t r0 = ((int64_t)blockIdx.x * 4 + wave_of()) * each;
   // lane i finds out about row r0 + i
   int cut = 1;
   if (lane < each && r0 + lane >= first && r0 + lane < last) cut = a.part_n[r0 + lane];
@@ -479,42 +548,17 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnLaunch a, int split
     const int at = __builtin_ctzll(todo);
     todo &= todo - 1;
     const int64_t row = r0 + at;
-    const int n = min(__builtin_amdgcn_readlane(cut, at), splits);
-    // lane s weighs split s
-    const float e = lane < n ? a.part_lse[lane * rows + row] : NEG_INF;
-    float top = e;
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-    const float base = top == NEG_INF ? 0.0f : top;
-    const float f = exp2_fast(e - base);
-    float sum = f;
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
-    const int w = W > 1 ? wave : 0, share = (n + W - 1) / W;
-    float acc[V] = {};
+    const int n = min(__builtin_amdgcn_readlane(cut, at), a.splits);
+    float base, sum, acc[V] = {};
+    const float f = split_weight(lane < n ? a.part_lse[lane * rows + row] : NEG_INF, base, sum);
     const float* src = a.part_o + row * DIM + V * lane;
 #pragma unroll 8
-    for (int s = w * share; s < min(n, (w + 1) * share); ++s) {
-      const float g = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), s));
+    for (int s = 0; s < n; ++s) {
+      const float g = lane_value(f, s);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] = fmaf(g, src[s * rows * DIM + i], acc[i]);
     }
-    if (W > 1) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) sm[wave][V * lane + i] = acc[i];
-      __syncthreads();
-      if (wave != 0) return;
-#pragma unroll
-      for (int x = 1; x < W; ++x)
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += sm[x][V * lane + i];
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    E* dst = (E*)a.out + row * DIM + V * lane;
-#pragma unroll
-    for (int i = 0; i < V; ++i) dst[i] = from_f32<E>(acc[i] * inv);
-    if (a.lse != nullptr && lane == 0)
-      a.lse[row] = sum == 0.0f ? NEG_INF : (base + __log2f(sum)) * LN2;
+    join_store<E, DIM>(a, row, acc, base, sum, lane);
   }
 }
 
@@ -538,18 +582,15 @@ template <typename E> hipError_t rows_dim(const AttnLaunch& L) {
   return L.dim == 64 ? rows_rb<E, 64>(L) : rows_rb<E, 128>(L);
 }
 
-// Four waves share a row where there are many splits of few rows; with many rows,
-// some of which were not split, a wave looks at four of them.
 template <typename E, int DIM> hipError_t join_go(const AttnLaunch& L) {
-  const int splits = L.splits;
   const int64_t rows = (int64_t)L.total * L.hq;
-  if (splits > 8 && rows <= 8192) {
-    hipLaunchKernelGGL((join_kernel<E, DIM, 4>), dim3((unsigned)rows), dim3(256), 0,
-                       (hipStream_t)L.stream, L, splits, 1);
+  if (rows * L.splits <= 16384) {  // reads every split's place, used or not: 8 MB at most
+    hipLaunchKernelGGL((join_few_kernel<E, DIM>), dim3((unsigned)rows), dim3(256), 0,
+                       (hipStream_t)L.stream, L);
   } else {
     const int each = rows <= 16384 ? 1 : 4;
-    hipLaunchKernelGGL((join_kernel<E, DIM, 1>), dim3((unsigned)((rows + 4 * each - 1) / (4 * each))),
-                       dim3(256), 0, (hipStream_t)L.stream, L, splits, each);
+    hipLaunchKernelGGL((join_kernel<E, DIM>), dim3((unsigned)((rows + 4 * each - 1) / (4 * each))),
+                       dim3(256), 0, (hipStream_t)L.stream, L, each);
   }
   return hipGetLastError();
 }
