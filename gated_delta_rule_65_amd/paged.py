@@ -111,6 +111,18 @@ def _same_device(dev, **tensors):
             _fail(f"{name} must be on {dev}")
 
 
+# torch's own lookup of the current stream: 0.2 us, where building a Stream object to
+# read its handle takes 1.9 of a short call's 8-12 us.  Builds without it take the object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(dev):
+    """The handle of torch's current stream on a GPU."""
+    if _raw_stream is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
 def _call(fn, args, dev):
     """Runs a library call with the tensors' device current; raises on an error."""
     if dev.index is None or dev.index == torch.cuda.current_device():
@@ -230,7 +242,7 @@ def page_tables(context_lens, new_lens, free_pages, block_table, page_size, num_
         stride, n, free.shape[0], cols, page_size, int(num_pages), tokens,
         out.slot_mapping.data_ptr(), out.positions.data_ptr(), out.cu_seqlens.data_ptr(),
         out.seq_lens.data_ptr(), out.pages_taken.data_ptr(),
-        torch.cuda.current_stream(dev).cuda_stream), dev)
+        _stream(dev)), dev)
     return out
 
 
@@ -266,7 +278,7 @@ def kv_append(k, v, k_cache, v_cache, slot_mapping):
     _call(lib.kda_kv_append, KvAppendArgs(
         _SIZEOF_APPEND, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         slot_mapping.data_ptr(), T, ks, vs, kp, vp, _DTYPES[dtype], hkv, dim, page_size, pages,
-        torch.cuda.current_stream(dev).cuda_stream), dev)
+        _stream(dev)), dev)
 
 
 def _rows_stride(name, t):
@@ -378,6 +390,6 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, scal
     a.q, a.k_cache, a.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
     a.block_table, a.cu_seqlens, a.seq_lens = block_table.data_ptr(), cu.data_ptr(), seq.data_ptr()
     a.out, a.lse = output.data_ptr(), None if lse is None else lse.data_ptr()
-    a.stream = torch.cuda.current_stream(dev).cuda_stream
+    a.stream = _stream(dev)
     _call(lib.kda_paged_attention, a, dev)
     return (output, lse) if return_lse else output
