@@ -531,35 +531,62 @@ template <typename E, int DIM> __global__ __launch_bounds__(256) void join_few_k
   join_store<E, DIM>(a, row, acc, base, sum, lane);
 }
 
-// Many rows, some of which were not split: a wave looks at `each` consecutive ones.
-template <typename E, int DIM>
-__global__ __launch_bounds__(256) void join_kernel(const AttnLaunch a, int each) {
-  constexpr int V = DIM / 64;
-  const int lane = threadIdx.x & 63;
+// Many rows, some of which were not split: 16 lanes share one.  The partials are asked
+// for with their lse, eight splits at a time.
+template <typename E, int DIM> __global__ __launch_bounds__(256) void join_kernel(const AttnLaunch a) {
+  constexpr int V = DIM / 16, AT_ONCE = 8;
+  const int lane = threadIdx.x & 63, at = lane & 15;
   const int64_t rows = (int64_t)a.total * a.hq;
+  const int64_t row = ((int64_t)blockIdx.x * 4 + wave_of()) * 4 + (lane >> 4);
   const int64_t first = (int64_t)min(max(a.cu[0], 0), a.total) * a.hq;
   const int64_t last = (int64_t)min(max(a.cu[a.n], 0), a.total) * a.hq;
-  const int64_t r0 = ((int64_t)blockIdx.x * 4 + wave_of()) * each;
-  // lane i finds out about row r0 + i
-  int cut = 1;
-  if (lane < each && r0 + lane >= first && r0 + lane < last) cut = a.part_n[r0 + lane];
-  uint64_t todo = __ballot(cut > 1);
-  while (todo != 0) {
-    const int at = __builtin_ctzll(todo);
-    todo &= todo - 1;
-    const int64_t row = r0 + at;
-    const int n = min(__builtin_amdgcn_readlane(cut, at), a.splits);
-    float base, sum, acc[V] = {};
-    const float f = split_weight(lane < n ? a.part_lse[lane * rows + row] : NEG_INF, base, sum);
-    const float* src = a.part_o + row * DIM + V * lane;
-#pragma unroll 8
-    for (int s = 0; s < n; ++s) {
-      const float g = lane_value(f, s);
+  const int cut = row >= first && row < last ? a.part_n[row] : 1;
+  const int n = cut > 1 ? min(cut, a.splits) : 0;
+  if (n == 0) return;  // a row's 16 lanes leave together
+  const float* src = a.part_o + row * DIM + V * at;
+  float x[AT_ONCE][V];
+  auto load = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = fmaf(g, src[s * rows * DIM + i], acc[i]);
+    for (int j = 0; j < AT_ONCE; ++j)
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 f = *(const float4*)(src + min(s + j, n - 1) * rows * DIM + i);
+        x[j][i] = f.x, x[j][i + 1] = f.y, x[j][i + 2] = f.z, x[j][i + 3] = f.w;
+      }
+  };
+  // lane i weighs the splits i, i + 16, i + 32 and i + 48
+  float f[4], top = NEG_INF, sum = 0.0f, acc[V] = {};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = at + 16 * k < n ? a.part_lse[(at + 16 * k) * rows + row] : NEG_INF;
+  load(0);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) top = fmaxf(top, f[k]);
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  const float base = top == NEG_INF ? 0.0f : top;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sum += f[k] = exp2_fast(f[k] - base);
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  for (int s = 0;;) {
+    const float w = s < 16 ? f[0] : s < 32 ? f[1] : s < 48 ? f[2] : f[3];
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {
+      const float g = __shfl(w, (s & 15) + j, 16);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = s + j < n ? fmaf(g, x[j][i], acc[i]) : acc[i];
     }
-    join_store<E, DIM>(a, row, acc, base, sum, lane);
+    s += AT_ONCE;
+    if (s >= n) break;
+    load(s);
   }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < V; i += 4)
+    store4((E*)a.out + row * DIM + V * at + i, acc[i] * inv, acc[i + 1] * inv, acc[i + 2] * inv,
+           acc[i + 3] * inv);
+  if (a.lse != nullptr && at == 0)
+    a.lse[row] = sum == 0.0f ? NEG_INF : (base + __log2f(sum)) * LN2;
 }
 
 template <typename E, int DIM, int RB> hipError_t rows_go(const AttnLaunch& L) {
@@ -588,9 +615,8 @@ template <typename E, int DIM> hipError_t join_go(const AttnLaunch& L) {
     hipLaunchKernelGGL((join_few_kernel<E, DIM>), dim3((unsigned)rows), dim3(256), 0,
                        (hipStream_t)L.stream, L);
   } else {
-    const int each = rows <= 16384 ? 1 : 4;
-    hipLaunchKernelGGL((join_kernel<E, DIM>), dim3((unsigned)((rows + 4 * each - 1) / (4 * each))),
-                       dim3(256), 0, (hipStream_t)L.stream, L, each);
+    hipLaunchKernelGGL((join_kernel<E, DIM>), dim3((unsigned)((rows + 15) / 16)), dim3(256), 0,
+                       (hipStream_t)L.stream, L);
   }
   return hipGetLastError();
 }
