@@ -202,6 +202,15 @@ def test_large_scores_and_growing_maximum():
                 attend(c, 16, scale=scale)
 
 
+@pytest.mark.parametrize("dtype,dim", [(BF, 128), (HF, 64), (FP, 128), (FP, 64)], ids=str)
+def test_many_rows_join_up_to_64_pieces(dtype, dim):
+    # 20 x 16 rows, cut into 1, 2, 8, 9, 16, 17, 31, 32, 33, 48, 49 and 64 pieces of 256
+    # keys or more, beside rows that are not cut and rows behind the batch
+    ctx = [256 * p + 3 for p in (1, 2, 8, 9, 16, 17, 31, 32, 33, 48, 49, 64)] + [0, 1, 5, 100, 255, 400, 511, 2]
+    c = R.make(ctx, [1] * len(ctx), 16, 1, dim, 64, dtype, seed=71, pad_rows=3)
+    check(c, 64, attend(c, 64, max_new_len=1, splits=64))
+
+
 def test_hint_and_splits_change_sums_only():
     c = R.make([700, 3, 90], [40, 1, 7], 8, 2, 128, 16, BF, seed=6)
     for hint in (None, 1, 7, 40, 1000):
