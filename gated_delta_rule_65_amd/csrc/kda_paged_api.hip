@@ -27,6 +27,22 @@ bool misaligned(std::initializer_list<const void*> ps, size_t a) {
   return false;
 }
 
+// Whether a buffer of `a` and one of `b` share bytes.
+struct Span {
+  const void* at;
+  int64_t bytes;
+};
+bool overlap(std::initializer_list<Span> a, std::initializer_list<Span> b) {
+  for (const Span& x : a)
+    for (const Span& y : b) {
+      const uintptr_t p = reinterpret_cast<uintptr_t>(x.at), q = reinterpret_cast<uintptr_t>(y.at);
+      if (p != 0 && q != 0 && x.bytes > 0 && y.bytes > 0 && p < q + (uintptr_t)y.bytes &&
+          q < p + (uintptr_t)x.bytes)
+        return true;
+    }
+  return false;
+}
+
 size_t elem_size(int dtype) { return dtype == KDA_F32 ? 4 : 2; }
 
 // What append and attention have in common: the pools.
@@ -200,10 +216,19 @@ KDA_API kda_status kda_page_tables(const kda_page_tables_args* a) {
                   a->cu_seqlens, a->seq_lens, a->pages_taken}, 4) ||
       misaligned({a->slot_mapping}, 8))
     FAIL(KDA_ERR_ARG, "index arrays must be aligned to their elements");
+  // the first workgroup writes lengths that the others may have yet to read
+  const int64_t n4 = 4 * (int64_t)a->n, stride = a->table_stride ? a->table_stride : a->max_pages;
+  const Span table = {a->block_table, a->n > 0 ? 4 * ((a->n - 1) * stride + a->max_pages) : 0};
+  const Span lens[] = {{a->context_lens, n4}, {a->new_lens, n4}, {a->free_pages, 4 * (int64_t)a->num_free}};
+  if (overlap({lens[0], lens[1], lens[2], table},
+              {{a->cu_seqlens, n4 + 4}, {a->seq_lens, n4}, {a->pages_taken, 4},
+               {a->slot_mapping, 8 * a->max_tokens}, {a->positions, 4 * a->max_tokens}}) ||
+      overlap({lens[0], lens[1], lens[2]}, {table}))
+    FAIL(KDA_ERR_ARG, "outputs must not overlap inputs (a step's seq_lens are not its context_lens)");
   kda::TablesLaunch L;
   L.context = a->context_lens; L.fresh = a->new_lens; L.free_pages = a->free_pages;
   L.table = a->block_table;
-  L.table_stride = a->table_stride ? a->table_stride : a->max_pages;
+  L.table_stride = stride;
   L.slots = a->slot_mapping; L.positions = a->positions;
   L.cu = a->cu_seqlens; L.seq = a->seq_lens; L.taken = a->pages_taken;
   L.max_tokens = a->max_tokens;

@@ -64,6 +64,7 @@ _SIZEOF_ATTENTION = ctypes.sizeof(PagedAttentionArgs)
 
 EXPORTS = ("kda_page_tables", "kda_kv_append", "kda_paged_attention_workspace_size",
            "kda_paged_attention")
+_MAX_INT = 2**31 - 1     # ctypes cuts what an int32 field does not hold
 _lib = None
 
 
@@ -197,16 +198,19 @@ def page_tables(context_lens, new_lens, free_pages, block_table, page_size, num_
     place (the entries of the pages taken; rows may lie apart); num_pages: pages of
     the cache.  max_tokens: room in the slot map, at least the step's new tokens (a
     captured step keeps its largest).  Returns a PageTables; ``out`` gives one to
-    write into (its slot_mapping then sets max_tokens)."""
+    write into (its slot_mapping then sets max_tokens), none of it memory of an input:
+    two that take turns serve steps that pass one's seq_lens on as context_lens."""
     if context_lens.dim() != 1:
         _fail("context_lens must be [n]")
     n = context_lens.shape[0]
     if free_pages.dim() != 1:
         _fail("free_pages must be [F]")
     stride, cols = _table(block_table, n)
-    page_size = int(page_size)
-    if page_size < 1:
-        _fail("page_size must be >= 1")
+    page_size, num_pages = int(page_size), int(num_pages)
+    if not 1 <= page_size <= _MAX_INT:
+        _fail("page_size must be >= 1 and below 2^31")
+    if not 0 <= num_pages <= _MAX_INT:
+        _fail("num_pages must be >= 0 and below 2^31")
     dev = block_table.device
     ctx = _int32(context_lens, n, "context_lens", dev)
     new = _int32(new_lens, n, "new_lens", dev)
@@ -239,7 +243,7 @@ def page_tables(context_lens, new_lens, free_pages, block_table, page_size, num_
     lib = _lib or load_library()
     _call(lib.kda_page_tables, PageTablesArgs(
         _SIZEOF_TABLES, ctx.data_ptr(), new.data_ptr(), free.data_ptr(), block_table.data_ptr(),
-        stride, n, free.shape[0], cols, page_size, int(num_pages), tokens,
+        stride, n, free.shape[0], cols, page_size, num_pages, tokens,
         out.slot_mapping.data_ptr(), out.positions.data_ptr(), out.cu_seqlens.data_ptr(),
         out.seq_lens.data_ptr(), out.pages_taken.data_ptr(),
         _stream(dev)), dev)
@@ -309,10 +313,15 @@ def _attention_args(q, k_cache, v_cache, block_table, n, scale, window, sinks, m
     window, sinks = int(window), int(sinks)
     if window < 0 or sinks < 0:
         _fail("window and sinks must be >= 0")
+    max_new_len, splits = int(max_new_len or 0), int(splits)
+    if max_new_len < 0:
+        _fail("max_new_len must be >= 0")
+    if not 0 <= splits <= 64:
+        _fail("splits must lie in [0, 64]")
     return PagedAttentionArgs(
         _SIZEOF_ATTENTION, None, None, None, None, None, None, None, None, None, 0, T,
         _rows_stride("q", q), kp, vp, stride, _DTYPES[dtype], n, hq, hkv, dim, page_size, pages, cols,
-        min(window, 1 << 30), min(sinks, 1 << 30), int(max_new_len or 0), int(splits),
+        min(window, 1 << 30), min(sinks, 1 << 30), min(max_new_len, 1 << 30), splits,
         float(dim ** -0.5 if scale is None else scale), None)
 
 

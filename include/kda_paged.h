@@ -53,10 +53,13 @@ extern "C" {
  * free_pages runs out (pages_taken[0] > num_free), the tokens left over get
  * slot -1 and their table entries -1.  A position past the table's width has no
  * page.  Pages given out are distinct as long as those in free_pages are.  Sums
- * and lengths stay below 2^31.
+ * and lengths stay below 2^31.  No output may share memory with an input: the
+ * seq_lens of one step serve the next as context_lens, but that step then needs
+ * a seq_lens of its own (a call with shared memory is refused).
  *
- * Errors: KDA_ERR_ARG (NULL or bad struct), KDA_ERR_SHAPE, KDA_ERR_UNSUPPORTED
- * (num_pages * page_size, max_pages * page_size or max_tokens above 2^30).
+ * Errors: KDA_ERR_ARG (NULL, bad struct, shared memory), KDA_ERR_SHAPE,
+ * KDA_ERR_UNSUPPORTED (num_pages * page_size, max_pages * page_size or max_tokens
+ * above 2^30).
  */
 typedef struct kda_page_tables_args {
   size_t struct_size;          /* = sizeof(kda_page_tables_args) */
@@ -82,7 +85,8 @@ kda_status kda_page_tables(const kda_page_tables_args *a);
 /*
  * kda_kv_append_args -- rows [T, Hkv, head_dim] of K and V copied to their cache
  * slots; a slot outside [0, num_pages * page_size) skips its token.  Slots are
- * distinct (of two equal ones, either token's bytes may land).
+ * distinct (of two equal ones, either token's bytes may land), and no slot is a
+ * row that the call reads.
  *
  * Errors: KDA_ERR_ARG (NULL, bad struct, misaligned), KDA_ERR_DTYPE,
  * KDA_ERR_SHAPE, KDA_ERR_UNSUPPORTED (head_dim other than 64 or 128, num_pages *
@@ -124,10 +128,10 @@ kda_status kda_kv_append(const kda_kv_append_args *a);
  * Scores, softmax statistics and sums are held in fp32; for 16-bit types the
  * probabilities are rounded to the input type for their product with V, and out
  * is rounded once.  A row that sees no key (a position below 0, no page) gets
- * zeros and lse = -inf, as does one whose scores are all -inf.  What lies at positions that a row does not see does not
- * reach it, be it infinite or NaN.  Rows of out and lse behind the last request
- * are left as they are.  A length beyond the table's width reads the table's
- * positions only.
+ * zeros and lse = -inf, as does one whose scores are all -inf.  What lies at
+ * positions that a row does not see does not reach it, be it infinite or NaN.
+ * Rows of out and lse behind the last request are left as they are.  A length
+ * beyond the table's width reads the table's positions only.
  *
  * Long key ranges are cut into splits that run in parallel and are joined in a
  * fixed order, so equal calls give equal bits; the count is chosen from sizes

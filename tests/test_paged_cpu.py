@@ -102,6 +102,24 @@ def test_tables_refusals(lib, fields, status):
     assert lib.kda_last_error()
 
 
+def test_tables_refuse_outputs_that_share_memory_with_inputs(lib):
+    # buffers apart from one another, then one moved to where it shares a few bytes with another
+    sizes = dict(context_lens=16, new_lens=16, free_pages=36, block_table=4 * (3 * 10 + 8), cu_seqlens=20,
+                 seq_lens=16, pages_taken=4, slot_mapping=800, positions=400)
+    at, place = FAKE, {}
+    for name, size in sizes.items():
+        place[name] = at
+        at += size + -size % 8
+    outs = ("cu_seqlens", "seq_lens", "pages_taken", "slot_mapping", "positions")
+    ins = ("context_lens", "new_lens", "free_pages", "block_table")
+    pairs = [(o, i) for o in outs for i in ins] + [("block_table", i) for i in ins[:3]]
+    for o, i in pairs:
+        for start in (place[i], place[i] + (sizes[i] - 4) // 8 * 8, place[i] - (sizes[o] - 4) // 8 * 8):
+            a = tables(**{**place, o: start}, table_stride=10)
+            assert lib.kda_page_tables(ctypes.byref(a)) == ARG, (o, i)
+            assert b"overlap" in lib.kda_last_error()
+
+
 @pytest.mark.parametrize("fields,status", [
     (dict(struct_size=8), ARG), (dict(dtype=7), DTYPE), (dict(hkv=0), SHAPE), (dict(page_size=0), SHAPE),
     (dict(num_pages=0), SHAPE), (dict(head_dim=96), UNSUP), (dict(num_pages=1 << 28), UNSUP),
@@ -229,6 +247,20 @@ def test_binding_append_and_tables_refusals():
             ((n, n, n, table, 16, 8), dict(out=P.PageTables(n, n, slots, n, n)), ValueError, "out.cu")):
         with pytest.raises(exc, match=match):
             P.page_tables(*args, **kw)
+
+
+def test_binding_refuses_sizes_that_int32_would_cut():
+    n, table = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 4, dtype=torch.int32)
+    for page, pages, match in ((2**32 + 16, 8, "page_size"), (16, 2**32 + 8, "num_pages"),
+                               (16, -1, "num_pages")):
+        with pytest.raises(ValueError, match=match):
+            P.page_tables(n, n, n, table, page, pages, max_tokens=4)
+    for change, match in ((dict(splits=2**32 + 1), "splits"), (dict(splits=65), "splits"),
+                          (dict(splits=-1), "splits"), (dict(max_new_len=-1), "max_new_len"),
+                          (dict(max_new_len=-2**32 + 1), "max_new_len"),
+                          (dict(max_new_len=2**32 + 1), "GPU")):
+        with pytest.raises(ValueError, match=match):
+            P.paged_attention(**{**cpu_case(), **change})
 
 
 def test_page_stride_of_interleaved_pools():
