@@ -60,6 +60,15 @@ template <int N> __device__ __forceinline__ void dma_wait() {
 // Every LDS read issued so far has returned.
 __device__ __forceinline__ void lds_wait() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
 
+// All waves of the workgroup come here, each with at most N vector-memory operations in
+// flight and no LDS read; LDS accesses stay on their side.
+template <int N> __device__ __forceinline__ void tile_barrier() {
+  dma_wait<N>();
+  lds_wait();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" : : : "memory");
+}
+
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
@@ -244,7 +253,9 @@ struct PageWindow {
     const int p0 = (int)fdiv(first, a.page), p1 = (int)fdiv(last, a.page);
     return (none >> (p0 - base)) & (~0ull >> (63 - (p1 - p0)));
   }
-  // The page at index `page` of the row (a lane's own, or a uniform one), -1 if none.
+  // The page at index `page` of the row (a lane's own, or a uniform one), -1 if none.  All
+  // lanes have to ask, with or without a use for it: one that is switched off hands out
+  // page 0 in place of its entry.
   __device__ __forceinline__ int at(int page) const {
     return __builtin_amdgcn_ds_bpermute(4 * (page - base), entry);
   }

@@ -137,7 +137,8 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(const AttnLaunch a) {
       if (t.base + KT > range.end || !(t.base >= range.lo || t.base + KT <= range.sink_end) ||
           pages.missing(a, t.base, last)) {
         const int key = t.base + l16;
-        t.valid = (uint32_t)__ballot(range.has(key) && pages.at((int)fdiv(key, a.page)) >= 0) & ALL;
+        const int page = pages.at((int)fdiv(key, a.page));  // of every lane's key
+        t.valid = (uint32_t)__ballot(range.has(key) && page >= 0) & ALL;
       }
       return t;
     };

@@ -128,7 +128,8 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
     if (base + KT > range.end || !(base >= range.lo || base + KT <= range.sink_end) ||
         pages.missing(a, base, last)) {
       const int key = base + lane;
-      valid = __ballot(range.has(key) && pages.at((int)fdiv(key, a.page)) >= 0);
+      const int page = pages.at((int)fdiv(key, a.page));  // of every lane's key
+      valid = __ballot(range.has(key) && page >= 0);
     }
     if (even && valid == ~0ull) {
       // one page per instruction: the addresses are scalar work
@@ -352,9 +353,7 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const AttnLaunch a) {
         base[j] = nbase[j];
       }
       // these tiles have landed for every wave, and every wave is done with the last
-      dma_wait<0>();
-      lds_wait();
-      __builtin_amdgcn_s_barrier();
+      tile_barrier<0>();
       load(i + PAIR, half ^ 1);
       if constexpr (!BUSY) continue;
 #pragma unroll

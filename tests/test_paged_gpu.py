@@ -139,6 +139,24 @@ def test_missing_pages_hold_no_key(dt, new):
     check(c, page, attend(c, page))
 
 
+@pytest.mark.parametrize("dt,new,cols", [(BF, 1, 0), (HF, 1, 0), (FP, 1, 0), (FP, 40, 0), (BF, 70, 0),
+                                         (HF, 200, 0), (FP, 300, 60)])
+def test_a_missing_last_page_that_holds_few_keys(dt, new, cols):
+    """The last page, begun but missing, at many places of the table."""
+    page = 16
+    for pages in (1, 2, 3, 9, 17, 18, 33):
+        L = page * (pages - 1) + 1 + pages % 3
+        if L < new:
+            continue
+        c = R.make([L - new], [new], 4, 2, 128, page, dt, seed=pages, extra_cols=2 + cols,
+                   holes=[(0, pages - 1)])
+        check(c, page, attend(c, page))
+        c.table[0, pages - 1] = c.k_cache.shape[0]     # an entry past the cache is no page either
+        got = attend(c, page, splits=3)
+        c.table[0, pages - 1] = -1
+        check(c, page, got)
+
+
 def test_positions_past_the_table_hold_no_key():
     """A table too narrow for the request: the positions that it lists are read."""
     for dt, new in ((BF, 1), (HF, 70), (FP, 5)):
