@@ -1,5 +1,5 @@
-// Paged attention of few rows per request (decode, short drafts) and of every fp32
-// call, and the join of split partials.
+// Paged attention of few rows per request (decode, short drafts; in fp32 also short
+// chunks), and the join of split partials.
 //
 // out = softmax(scale q K^T) V over a request's visible keys, in one pass with
 // the running maximum m and sum l of the softmax (exponents in base 2, the scale
@@ -14,9 +14,7 @@
 // starts or joins.  256 ragged decode requests (1.7 GB of keys and values): 311 us, 5.5
 // TB/s, where a plain read reaches 6.3; with tiles of 32 keys and one workgroup per
 // unit it was 440 us, and a third buffer, a single one, or shorter splits change
-// nothing.  fp32 is bound by its products (16 x 16 x 4, full precision) and by the
-// start of a workgroup, and by the way of the keys from L2: 840 tokens in three chunks
-// 40 us (the call 44 us, with 16 rows a workgroup 64 us).
+// nothing.
 #include "kda_attn.hpp"
 
 namespace kda {
@@ -596,7 +594,7 @@ template <typename E, int DIM, int RB> hipError_t rows_go(const AttnLaunch& L) {
     hipLaunchKernelGGL((rows_kernel<E, DIM, RB, true>),
                        dim3((unsigned)(L.n * L.hkv), (unsigned)L.splits), dim3(64 * WAVES), 0,
                        (hipStream_t)L.stream, L);
-  } else {
+  } else if constexpr (sizeof(E) == 4 && RB == 2) {  // the only one that is asked for
     const int64_t tiles = (int64_t)L.total * L.group / (16 * RB) + L.n;
     hipLaunchKernelGGL((rows_kernel<E, DIM, RB, false>),
                        dim3((unsigned)(tiles * L.hkv), (unsigned)L.splits), dim3(64 * WAVES), 0,

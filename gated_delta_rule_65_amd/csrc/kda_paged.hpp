@@ -74,11 +74,14 @@ struct AttnLaunch {
   int tile_waves;          // tiles kernel: waves of 32 rows (4 or 8); 0: the rows kernel runs
   int row_blocks;          // rows kernel: 16-row blocks per wave (1 or 2)
   int by_request;          // rows kernel: a workgroup per request, not per row tile
+  int chunks;              // the fp32 chunks kernel runs
   int splits, min_keys;    // splits of a visit at most, and keys of one at least
   void* stream;
 };
+constexpr int CHUNK_ROWS = 128;  // rows of a workgroup of the fp32 chunks
 hipError_t launch_attn_rows(const AttnLaunch& L);
 hipError_t launch_attn_tiles(const AttnLaunch& L);
+hipError_t launch_attn_chunks(const AttnLaunch& L);
 hipError_t launch_attn_join(const AttnLaunch& L);
 
 // Stores the calling thread's error text (kda_last_error) and returns status.

@@ -141,8 +141,8 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
   int64_t keys = L.key_capacity;
   if (L.window > 0 && (int64_t)L.window + L.sinks + most_new < keys)
     keys = (int64_t)L.window + L.sinks + most_new;
-  // The rows kernel serves calls whose requests have up to 32 rows per kv head, and
-  // fp32; else all requests go through the matrix tiles, the short ones beside the
+  // The rows kernel serves calls whose requests have up to 32 rows per kv head, and short
+  // fp32 ones; else all requests go through matrix tiles, the short ones beside the
   // chunks in one launch (33 mixed requests: 86 us against 101 us in a launch each, both
   // with a join 4 us slower than now).
   const int64_t most_rows = most_new * L.group, rows = a->total_tokens * a->hq;
@@ -150,6 +150,12 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
   const bool tiles = a->dtype != KDA_F32 && most_rows > 32;
   L.row_blocks = most_rows > 16 ? 2 : 1;
   L.by_request = most_rows <= 32;
+  // fp32 requests of 256 rows and more, on average, on 512 keys or more: workgroups of 128
+  // rows (2048 tokens on 8192 keys, 8 heads on 2: 560 us against 690 us; 3 chunks of 840
+  // tokens: 40.6 us against 44.2 us; but 8 requests of 128 rows on 2032 keys: 70 us against
+  // 45 us, 40 of 33 rows: 420 us against 316 us, 200 tokens alone: 26.9 us against 19.6 us).
+  L.chunks = a->dtype == KDA_F32 && !L.by_request && keys >= 512 &&
+             group_rows >= (int64_t)a->n * 2 * kda::CHUNK_ROWS;
   // Eight waves (256 rows) a workgroup where key ranges are long and the rows fill the
   // chip with them, else four: kda_attn_tiles.hip says why, with both sides measured.
   L.tile_waves = !tiles ? 0 : keys >= 32768 && ceil_div(group_rows, 256) * a->hkv >= 256 ? 8 : 4;
@@ -166,8 +172,10 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
     L.min_keys = units + (int64_t)a->n * a->hkv >= 2048 ? 2048 : units >= 256 ? 1024 : 512;
     grid = units >= (L.tile_waves == 8 ? 256 : 512) * (a->n > 1 ? 3 : 1) ? 0 : units >= 256 ? 8192 : 1024;
   } else {
-    units = L.by_request ? (int64_t)a->n * a->hkv : ceil_div(group_rows, 16 * L.row_blocks) * a->hkv;
-    L.min_keys = units >= 1024 ? 2048 : units >= 256 ? 1024 : 256;
+    // (chunks: with 32, 64, 96 and 128 keys at least the 840 tokens take 46, 40, 43 and 51 us)
+    units = L.by_request ? (int64_t)a->n * a->hkv
+                         : ceil_div(group_rows, L.chunks ? kda::CHUNK_ROWS : 16 * L.row_blocks) * a->hkv;
+    L.min_keys = units >= 1024 ? 2048 : units >= 256 ? 1024 : L.chunks ? 64 : 256;
     grid = L.by_request ? 16384 : 2048;
   }
   int64_t want = a->splits > 0 ? a->splits : units > 0 ? grid / units : 1;
@@ -313,7 +321,9 @@ KDA_API kda_status kda_paged_attention(const kda_paged_attention_args* a) {
     L.part_n = (int32_t*)(ws + p.o_bytes + p.lse_bytes);
   }
   L.stream = a->stream;
-  hipError_t e = L.tile_waves > 0 ? kda::launch_attn_tiles(L) : kda::launch_attn_rows(L);
+  hipError_t e = L.tile_waves > 0 ? kda::launch_attn_tiles(L)
+                 : L.chunks       ? kda::launch_attn_chunks(L)
+                                  : kda::launch_attn_rows(L);
   if (e == hipSuccess && need > 0) e = kda::launch_attn_join(L);
   if (e != hipSuccess) FAIL(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
   return (kda_status)kda::set_ok();

@@ -325,6 +325,64 @@ def test_wide_tiles_keep_hidden_values_out(name):
     check_rows(c, page, attend(c, page, window, sinks), window, sinks)
 
 
+# fp32 requests of 256 rows and more on average, tables of 2048 positions:
+# context, new, hq, hkv, dim, page, window, sinks, holes
+FP32_CHUNKS = {
+    "one_chunk": ([0], [300], 4, 4, 128, 16, 0, 0, ()),
+    "ragged_groups_of_four": ([700, 3, 64], [90, 257, 128], 8, 2, 128, 48, 0, 0, ()),
+    "groups_of_three_64_channels": ([0, 511, 9], [129, 1, 400], 6, 2, 64, 20, 0, 0, ()),
+    "empty_requests": ([5, 0, 600, 0], [0, 500, 1, 0], 12, 1, 128, 64, 0, 0, ()),
+    "window_and_sinks": ([900, 0], [200, 270], 4, 2, 128, 16, 77, 5, ()),
+    "window_below_a_tile": ([33], [300], 2, 1, 64, 16, 9, 0, ()),
+    "sinks_past_a_tile": ([500], [150], 4, 2, 64, 32, 40, 70, ()),
+    "page_of_one": ([40], [260], 1, 1, 128, 1, 0, 0, ()),
+    "page_of_three_window": ([400], [140], 6, 3, 128, 3, 90, 4, ()),
+    "pages_missing": ([300, 0], [170, 130], 4, 2, 128, 16, 0, 0, ((0, 0), (0, 7), (0, 19), (1, 0), (1, 8))),
+}
+
+
+def fp32_chunks(name):
+    ctx, new, hq, hkv, dim, page, window, sinks, holes = FP32_CHUNKS[name]
+    c = R.make(ctx, new, hq, hkv, dim, page, FP, seed=23, pad_rows=3, holes=holes)
+    assert int(c.cu[-1]) * (hq // hkv) >= 256 * len(ctx)
+    table = torch.full((len(ctx), -(-2048 // page)), -1, dtype=torch.int32)
+    table[:, :c.table.shape[1]] = c.table
+    c.table = table
+    return c, page, window, sinks
+
+
+@pytest.mark.parametrize("splits", [0, 1, 5])
+@pytest.mark.parametrize("name", list(FP32_CHUNKS))
+def test_fp32_chunks_match_64_bits(name, splits):
+    c, page, window, sinks = fp32_chunks(name)
+    check(c, page, attend(c, page, window, sinks, splits=splits), window, sinks)
+
+
+@pytest.mark.parametrize("name", ["one_chunk", "ragged_groups_of_four", "window_and_sinks", "pages_missing"])
+def test_fp32_chunks_keep_hidden_values_out(name):
+    c, page, window, sinks = fp32_chunks(name)
+    for i in range(len(c.keys)):
+        L = int(c.seq[i])
+        for pos, what, rows, cache in ((L - 1, float("nan"), c.values, c.v_cache),
+                                       (L - 40, float("inf"), c.values, c.v_cache),
+                                       (L - 2, float("nan"), c.keys, c.k_cache),
+                                       (L - 3, float("inf"), c.keys, c.k_cache)):
+            if c.table[i, pos // page] >= 0:
+                rows[i][pos, 0, 3] = what
+                cache[int(c.table[i, pos // page]), 0, pos % page, 3] = what
+    check_rows(c, page, attend(c, page, window, sinks), window, sinks, count=60)
+
+
+def test_fp32_chunks_at_negative_positions_and_past_the_table():
+    c, page, _, _ = fp32_chunks("one_chunk")
+    c.seq[0] = 300 - 37             # the first 37 rows lie before the request's first key
+    check(c, page, attend(c, page))
+    c.seq[0] = 300
+    c.table = c.table[:, :32].contiguous()
+    c.table[0, 11:] = -1            # 176 positions have a page
+    check(c, page, attend(c, page, splits=3))
+
+
 def small_reference(q, k, v, pos, key_pos, window, sinks, scale):
     """One row's output from its visible keys, in 64 bits."""
     see = (key_pos <= pos) & ((pos - key_pos < window) | (key_pos < sinks))
