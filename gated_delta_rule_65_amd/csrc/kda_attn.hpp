@@ -94,7 +94,6 @@ template <typename E> struct Half;
 template <> struct Half<bf16> {
   typedef bf16x8_t frag;
   typedef bf16x4_t quad;
-  static constexpr uint32_t EXP = 0x7f807f80u, CARRY = 0x00800080u;
   static constexpr float P_BIAS = 0.0f;
   static __device__ __forceinline__ f32x4_t mma16(frag a, frag b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -113,7 +112,6 @@ template <> struct Half<bf16> {
 template <> struct Half<_Float16> {
   typedef f16x8_t frag;
   typedef _Float16 quad __attribute__((ext_vector_type(4)));
-  static constexpr uint32_t EXP = 0x7c007c00u, CARRY = 0x04000400u;
   // Probabilities are scaled by 2^6 so that small ones stay normal numbers of
   // fp16 (the largest is 2^(6 + LAG), well inside its range).
   static constexpr float P_BIAS = 6.0f;
@@ -133,12 +131,6 @@ template <> struct Half<_Float16> {
     return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
   }
 };
-
-// Whether any of the piece's eight 16-bit values is an infinity or a NaN.
-template <typename E> __device__ __forceinline__ uint32_t nonfinite16(uint4 u) {
-  const uint32_t m = Half<E>::EXP, c = Half<E>::CARRY;
-  return (((u.x & m) + c) | ((u.y & m) + c) | ((u.z & m) + c) | ((u.w & m) + c)) & 0x80008000u;
-}
 
 // The request and row tile of a workgroup.  Request i's tiles start at index
 // floor(cu[i] G / ROWS) + i, which leaves it at least ceil(len G / ROWS) of them,
@@ -295,10 +287,6 @@ __device__ __forceinline__ float max_quarter(float x) {
 __device__ __forceinline__ float sum_quarter(float x) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return sum_half(__uint_as_float(r[0]) + __uint_as_float(r[1]));
-}
-
-__device__ __forceinline__ void store2(float* p, float a, float b) {
-  *reinterpret_cast<float2*>(p) = make_float2(a, b);
 }
 
 }  // namespace kda

@@ -71,10 +71,10 @@ struct AttnLaunch {
   FastDiv page, gdiv, hdiv;  // by the page size, the group, hkv
   int window, sinks;       // window 0: every earlier key
   float scale;
-  int tile_waves;          // tiles kernel: waves of 32 rows (4 or 8); 0: the rows kernel runs
+  int tile_waves;          // tiles kernel: waves of 32 rows (4 or 8); 0: another one runs
   int row_blocks;          // rows kernel: 16-row blocks per wave (1 or 2)
   int by_request;          // rows kernel: a workgroup per request, not per row tile
-  int chunks;              // the fp32 chunks kernel runs
+  int chunks;              // the fp32 chunks kernel runs, not the rows kernel
   int splits, min_keys;    // splits of a visit at most, and keys of one at least
   void* stream;
 };
