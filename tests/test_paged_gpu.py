@@ -636,3 +636,40 @@ def test_captured_step_replays_match_eager():
         assert torch.equal(out, eout) and torch.equal(table, etab)
         assert torch.equal(kc, ekv[0]) and torch.equal(vc, ekv[1])
         assert all(torch.equal(a, b) for a, b in zip(room, etabs))
+
+
+def test_two_captured_calls_and_two_streams_without_a_workspace():
+    """Split calls that allocate their scratch: in two graphs, replayed in turn with eager
+    calls between, and at once on two streams."""
+    from test_graphs_gpu import capture
+    cases = [R.make([1500, 3], [1, 1], 8, 2, 128, 16, BF, seed=31),
+             R.make([900], [300], 4, 2, 128, 16, FP, seed=32)]
+    args = [[x.to(DEV) for x in (c.q, c.k_cache, c.v_cache, c.table, c.cu, c.seq)] for c in cases]
+    outs = [torch.zeros_like(a[0]) for a in args]
+    call = lambda i, o: paged.paged_attention(*args[i], output=o, splits=4)
+    for a in args:
+        assert paged.paged_attention_workspace_bytes(a[0], a[1], a[2], a[3], splits=4) > 0
+    graphs = [capture(lambda i=i: call(i, outs[i])) for i in range(2)]
+    ref = []
+    for i, c in enumerate(cases):
+        got = attend(c, 16, splits=4)
+        check(c, 16, got)
+        ref.append(got[0].to(DEV))
+    for r in range(4):
+        print("replays in turn", r, flush=True)
+        for i in (r % 2, 1 - r % 2):
+            outs[i].fill_(5)
+            graphs[i].replay()
+            eager = call(1 - i, torch.empty_like(outs[1 - i]))
+            assert torch.equal(eager, ref[1 - i])
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, e) for o, e in zip(outs, ref))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(call(i, torch.empty_like(outs[i])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref[i]) for i in range(2) for o in got[i])
