@@ -5,9 +5,10 @@
 // requests 1024 at a time, with a prefix sum of (new tokens, missing pages) in LDS,
 // until it has placed all of its own.  Every workgroup repeats the walk, which takes a
 // scan per 1024 requests, and so needs no second launch.  A new page is entered by
-// the token that opens it, and its id comes from the free list, never from the
-// table, so workgroups do not depend on one another.  Bound by latency: 256 requests
-// of one token 3.9 us, 1000 requests with 93766 tokens 5.6 us.
+// the token that opens it, or by the first workgroup where that token lies past the
+// slot map's room, and its id comes from the free list, never from the table, so
+// workgroups do not depend on one another.  Bound by latency: 256 requests of one
+// token 3.9 us, 1000 requests with 93766 tokens 5.6 us.
 //
 // Append.  A copy of 16-byte pieces, bound by HBM: 32768 tokens of 8 heads of 128 fp16
 // channels (134 MB read, 134 MB written) 53 us, 5.0 TB/s; a large copy reaches 4.8.
@@ -21,6 +22,12 @@ constexpr int NT = 1024;
 
 __device__ __forceinline__ uint32_t pdiv(uint32_t t, const FastDiv& f) {
   return __umulhi(2u * t, f.mul) >> f.shift;
+}
+// Pages of t tokens.
+__device__ __forceinline__ int pages_of(uint32_t t, const FastDiv& f) {
+  t &= 0x7fffffffu;
+  const uint32_t p = pdiv(t, f);
+  return (int)(p + (p * f.d < t));
 }
 
 __global__ __launch_bounds__(NT) void page_tables_kernel(const TablesLaunch a) {
@@ -39,10 +46,9 @@ __global__ __launch_bounds__(NT) void page_tables_kernel(const TablesLaunch a) {
       ctx = max(a.context[i], 0);
       fresh = max(a.fresh[i], 0);
     }
-    const int have = (int)pdiv((uint32_t)ctx, a.page) + (pdiv((uint32_t)ctx, a.page) * a.page.d < (uint32_t)ctx);
+    const int have = pages_of((uint32_t)ctx, a.page);
     const uint32_t total = (uint32_t)ctx + (uint32_t)fresh;
-    const uint32_t td = total & 0x7fffffffu;
-    const int need = (int)pdiv(td, a.page) + (pdiv(td, a.page) * a.page.d < td) - have;
+    const int need = pages_of(total, a.page) - have;
     // inclusive sums over the wave, then over the waves
     int x = fresh, y = need;
 #pragma unroll
@@ -105,6 +111,23 @@ __global__ __launch_bounds__(NT) void page_tables_kernel(const TablesLaunch a) {
       }
       a.slots[t] = (uint32_t)id < (uint32_t)a.num_pages ? (int64_t)id * a.page.d + off : -1;
       if (a.positions != nullptr) a.positions[t] = pos;
+    }
+    if (__builtin_expect(blockIdx.x == 0 && tok_base + sx > a.max_tokens, 0)) {
+      // the pages [late, end) of the lane's request open past the room, where no thread has
+      // their token: the wave goes through its requests with such pages, 64 pages at a time
+      const int64_t left = a.max_tokens - (tok_base + bx + x - fresh);  // room for its tokens
+      const int late = pages_of((uint32_t)ctx + (uint32_t)min((int64_t)fresh, max(left, (int64_t)0)), a.page);
+      const int end = min(have + need, a.max_pages);
+      for (uint64_t some = __ballot(late < end); some != 0; some &= some - 1) {
+        const int l = __builtin_ctzll(some);
+        const int last = __shfl(end, l), held = __shfl(have, l);
+        const int64_t first = __shfl((int)(page_base + by + y - need), l);
+        int32_t* row = a.table + (int64_t)(i - lane + l) * a.table_stride;
+        for (int p = __shfl(late, l) + lane; p < last; p += 64) {
+          const int64_t f = first + (p - held);
+          row[p] = f >= 0 && f < a.num_free ? a.free_pages[f] : -1;
+        }
+      }
     }
     tok_base += s_cu[NT];
     page_base += sy;

@@ -49,7 +49,9 @@ extern "C" {
  *   slot_mapping[x] = its slot, -1 where it has no page
  *   pages_taken[0] = pages needed in all
  *
- * Entries of positions and slot_mapping behind the last new token are -1.  When
+ * Entries of positions and slot_mapping behind the last new token are -1.  New tokens
+ * past max_tokens have no entry in either; the other outputs, and the pages entered in
+ * block_table, are the whole step's all the same.  When
  * free_pages runs out (pages_taken[0] > num_free), the tokens left over get
  * slot -1 and their table entries -1.  A position past the table's width has no
  * page.  Pages given out are distinct as long as those in free_pages are.  Sums

@@ -486,6 +486,23 @@ def test_tables_out_of_pages_bad_entries_and_narrow_tables():
             assert torch.equal(g, r), what
 
 
+@pytest.mark.parametrize("name", list(TABLES) + ["one_long_request", "few_tokens_behind_a_long_one"])
+def test_tables_enter_the_pages_of_tokens_past_the_room(name):
+    """A slot map shorter than the step: the tables, offsets and counts are the whole step's."""
+    ctx, new, page = {**TABLES, "one_long_request": ([5], [70000], 1),
+                      "few_tokens_behind_a_long_one": ([3, 0, 9], [9000, 2, 40], 4)}[name]
+    free, table, num_pages = tables_args(ctx, new, page)
+    total = sum(new)
+    for f, t in ((free, table), (free[:len(free) // 2], table),
+                 (free, table[:, :max(table.shape[1] // 2, 1)].contiguous())):
+        for room in sorted({0, min(1, total), total // 3, max(total - 1, 0)}):
+            print("tables", name, "room", room, flush=True)
+            got = run_tables(ctx, new, f, t, page, num_pages, room)
+            ref = R.tables(ctx, new, f, t, page, num_pages, total)
+            for g, r, what in zip(got, ref, ("cu", "seq", "slots", "positions", "taken", "table")):
+                assert torch.equal(g, r[:room] if what in ("slots", "positions") else r), what
+
+
 def test_tables_in_a_strided_table_and_given_outputs():
     ctx, new, page = [10, 40, 0], [30, 30, 50], 16
     free, table, num_pages = tables_args(ctx, new, page)
