@@ -325,17 +325,20 @@ def _attention_args(q, k_cache, v_cache, block_table, n, scale, window, sinks, m
         float(dim ** -0.5 if scale is None else scale), None)
 
 
+def _workspace_bytes(lib, a):
+    nbytes = ctypes.c_size_t(0)
+    st = lib.kda_paged_attention_workspace_size(ctypes.byref(a), ctypes.byref(nbytes))
+    if st != KDA_OK:
+        _raise(lib, st)
+    return nbytes.value
+
+
 def paged_attention_workspace_bytes(q, k_cache, v_cache, block_table, window=0, sinks=0,
                                     max_new_len=None, splits=0):
     """Workspace bytes that paged_attention needs for tensors of these shapes."""
     a = _attention_args(q, k_cache, v_cache, block_table, block_table.shape[0], None, window,
                         sinks, max_new_len, splits)
-    lib = load_library()
-    nbytes = ctypes.c_size_t(0)
-    st = lib.kda_paged_attention_workspace_size(ctypes.byref(a), ctypes.byref(nbytes))
-    if st != KDA_OK:
-        _raise(lib, st)
-    return int(nbytes.value)
+    return _workspace_bytes(load_library(), a)
 
 
 def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, scale=None, window=0,
@@ -353,14 +356,16 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, scal
     cu_seqlens[n] are left as they are (undefined where the output is allocated here).
 
     max_new_len: the longest request's new tokens, a planning hint (1 for decode; taken
-    from cu_seqlens when that is a host tensor); results do not depend on it.
+    from cu_seqlens when that is a host tensor, unless a given workspace is too small for
+    the plan that it leads to); results do not depend on it.
     splits: 0 lets the library cut long key ranges; else at most that many pieces.
     workspace: optional scratch of paged_attention_workspace_bytes(), for one call at
     a time.  Returns out [T, Hq, D], or (out, lse [T, Hq] fp32) with return_lse."""
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         _fail("cu_seqlens must be [n + 1]")
     n = cu_seqlens.shape[0] - 1
-    if max_new_len is None and n > 0 and cu_seqlens.device.type == "cpu":
+    own_hint = max_new_len is None and n > 0 and cu_seqlens.device.type == "cpu"
+    if own_hint:
         max_new_len = max(0, int((cu_seqlens[1:] - cu_seqlens[:-1]).max()))
     a = _attention_args(q, k_cache, v_cache, block_table, n, scale, window, sinks, max_new_len,
                         splits)
@@ -387,12 +392,11 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, scal
         lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
     lib = _lib or load_library()
     if workspace is None:
-        nbytes = ctypes.c_size_t(0)
-        st = lib.kda_paged_attention_workspace_size(ctypes.byref(a), ctypes.byref(nbytes))
-        if st != KDA_OK:
-            _raise(lib, st)
-        if nbytes.value:
-            workspace = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+        nbytes = _workspace_bytes(lib, a)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif own_hint and _workspace_bytes(lib, a) > workspace.numel() * workspace.element_size():
+        a.max_new_len = 0       # its size was asked for without the offsets
     if workspace is not None:
         a.workspace = workspace.data_ptr()
         a.workspace_bytes = workspace.numel() * workspace.element_size()

@@ -263,6 +263,30 @@ def test_binding_refuses_sizes_that_int32_would_cut():
             P.paged_attention(**{**cpu_case(), **change})
 
 
+@pytest.mark.parametrize("cols", [100, 514, 8192])
+@pytest.mark.parametrize("new", [1, 3, 40])
+@pytest.mark.parametrize("n", [1, 4, 16, 70])
+def test_a_workspace_of_the_queried_size_serves_the_call(lib, monkeypatch, n, new, cols):
+    """Host offsets give the call a hint that the size query did not have, or had by hand."""
+    calls = []
+    monkeypatch.setattr(P, "_on_gpu", lambda dev: None)
+    monkeypatch.setattr(P, "_stream", lambda dev: 0)
+    monkeypatch.setattr(P, "_call", lambda fn, args, dev: calls.append(args))
+    q = torch.zeros(n * new, 32, 128, dtype=torch.bfloat16)
+    kc = torch.zeros(1, 8, 16, 128, dtype=torch.bfloat16)
+    table = torch.zeros(n, cols, dtype=torch.int32)
+    seq, cu = torch.zeros(n, dtype=torch.int32), torch.arange(0, n * new + 1, new)
+    for asked, given in ((None, None), (new, new), (new, None)):
+        size = P.paged_attention_workspace_bytes(q, kc, kc, table, max_new_len=asked)
+        for workspace in (torch.zeros(size, dtype=torch.uint8), None):
+            P.paged_attention(q, kc, kc, table, cu, seq, max_new_len=given, workspace=workspace)
+            a, need = calls.pop(), ctypes.c_size_t(0)
+            assert lib.kda_paged_attention_workspace_size(ctypes.byref(a), ctypes.byref(need)) == B.KDA_OK
+            assert need.value <= a.workspace_bytes, (asked, given)
+            if workspace is None and given is None:
+                assert a.max_new_len == new                # no need to do without the hint
+
+
 def test_page_stride_of_interleaved_pools():
     pool = torch.zeros(5, 2, 3, 16, 64, dtype=torch.bfloat16)
     assert P._page_stride("k_cache", pool[:, 0]) == 2 * 3 * 16 * 64

@@ -236,6 +236,20 @@ def test_hint_and_splits_change_sums_only():
             check(c, 16, attend(c, 16, max_new_len=hint, splits=splits))
 
 
+@pytest.mark.parametrize("asked", [None, 1])
+def test_a_workspace_of_the_queried_size_with_host_offsets(asked):
+    """Host offsets tell the call that these are single tokens; the query knew, or did not."""
+    c = R.make([300 + 7 * i for i in range(16)], [1] * 16, 32, 8, 128, 16, BF, seed=14, extra_cols=490)
+    args = [x.to(DEV) for x in (c.q, c.k_cache, c.v_cache, c.table)]
+    ws = torch.empty(paged.paged_attention_workspace_bytes(*args, max_new_len=asked), dtype=torch.uint8,
+                     device=DEV)
+    assert ws.numel() > 0
+    print("workspace", asked, ws.numel(), flush=True)
+    out, lse = paged.paged_attention(*args, c.cu, c.seq, return_lse=True, workspace=ws)
+    torch.cuda.synchronize()
+    check(c, 16, (out.cpu(), lse.cpu()))
+
+
 def test_many_requests_and_heads_that_are_no_power_of_two():
     """More requests than one look at the offsets covers, in both kernels."""
     ctx = [(37 * i) % 60 for i in range(150)]
