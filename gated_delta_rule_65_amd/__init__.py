@@ -9,7 +9,7 @@ does not load the library; the first call does, and raises if it is missing.
 _EXPORTS = ("KdaError", "chunk_kda", "kda_decode", "chunk_stages", "library_path",
             "load_library")
 _PAGED = ("PageTables", "page_tables", "kv_append", "paged_attention",
-          "paged_attention_workspace_bytes")
+          "paged_attention_workspace_bytes", "PAGED_ATTENTION_WORKSPACE_MAX")
 
 
 def __getattr__(name):

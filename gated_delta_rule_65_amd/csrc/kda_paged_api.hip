@@ -190,6 +190,8 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
     p.lse_bytes = ((size_t)L.splits * rows * 4 + 15) / 16 * 16;
     p.n_bytes = ((size_t)rows * 4 + 15) / 16 * 16;
   }
+  // at most 2^30 of partials, a 64th of it of log-sum-exps and, two splits or more, half
+  // of that of counts: KDA_PAGED_ATTENTION_WORKSPACE_MAX
   need = p.o_bytes + p.lse_bytes + p.n_bytes;
   return KDA_OK;
 }

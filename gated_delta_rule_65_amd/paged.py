@@ -64,6 +64,8 @@ _SIZEOF_ATTENTION = ctypes.sizeof(PagedAttentionArgs)
 
 EXPORTS = ("kda_page_tables", "kda_kv_append", "kda_paged_attention_workspace_size",
            "kda_paged_attention")
+# Workspace bytes that serve every paged_attention call (kda_paged.h).
+PAGED_ATTENTION_WORKSPACE_MAX = (1 << 30) + (1 << 25)
 _MAX_INT = 2**31 - 1     # ctypes cuts what an int32 field does not hold
 _lib = None
 
@@ -335,7 +337,10 @@ def _workspace_bytes(lib, a):
 
 def paged_attention_workspace_bytes(q, k_cache, v_cache, block_table, window=0, sinks=0,
                                     max_new_len=None, splits=0):
-    """Workspace bytes that paged_attention needs for tensors of these shapes."""
+    """Workspace bytes that paged_attention needs for tensors of these shapes.  Smaller ones
+    may be cut into more pieces and need more; PAGED_ATTENTION_WORKSPACE_MAX bytes serve
+    every call.  The pieces follow the table's width: a step of short requests asks for
+    less over the columns in use, block_table[:, :m]."""
     a = _attention_args(q, k_cache, v_cache, block_table, block_table.shape[0], None, window,
                         sinks, max_new_len, splits)
     return _workspace_bytes(load_library(), a)
@@ -359,8 +364,8 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, scal
     from cu_seqlens when that is a host tensor, unless a given workspace is too small for
     the plan that it leads to); results do not depend on it.
     splits: 0 lets the library cut long key ranges; else at most that many pieces.
-    workspace: optional scratch of paged_attention_workspace_bytes(), for one call at
-    a time.  Returns out [T, Hq, D], or (out, lse [T, Hq] fp32) with return_lse."""
+    workspace: optional scratch of paged_attention_workspace_bytes() for these shapes, or
+    of PAGED_ATTENTION_WORKSPACE_MAX for any, for one call at a time.  Returns out [T, Hq, D], or (out, lse [T, Hq] fp32) with return_lse."""
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         _fail("cu_seqlens must be [n + 1]")
     n = cu_seqlens.shape[0] - 1

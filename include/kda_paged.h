@@ -173,7 +173,15 @@ typedef struct kda_paged_attention_args {
 } kda_paged_attention_args;
 
 /* Workspace bytes of the call (0 is possible).  Reads only sizes, window, sinks,
- * max_new_len and splits. */
+ * max_new_len and splits.
+ *
+ * The need follows the plan of these very sizes: with splits = 0 fewer tokens or requests
+ * may be cut into more pieces and need more bytes, so a workspace asked for one shape is
+ * not one for smaller shapes.  KDA_PAGED_ATTENTION_WORKSPACE_MAX bytes serve every call.
+ * The pieces follow the table's width (max_pages), which is all that the host knows of the
+ * lengths: a step whose requests are short asks for less over the columns that they use
+ * (a smaller max_pages with the same table_stride), and one with splits = 1 for nothing. */
+#define KDA_PAGED_ATTENTION_WORKSPACE_MAX (((size_t)1 << 30) + ((size_t)1 << 25))
 kda_status kda_paged_attention_workspace_size(const kda_paged_attention_args *a, size_t *bytes);
 kda_status kda_paged_attention(const kda_paged_attention_args *a);
 

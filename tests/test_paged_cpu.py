@@ -185,6 +185,40 @@ def test_workspace_follows_the_splits(lib):
     assert workspace(lib, splits=0, max_pages=1 << 16, total_tokens=2) > 0
 
 
+def test_one_workspace_serves_every_shape(lib, tmp_path):
+    src = tmp_path / "m.c"
+    src.write_text('#include <stdio.h>\n#include "kda_paged.h"\n'
+                   'int main(void) { printf("%zu", KDA_PAGED_ATTENTION_WORKSPACE_MAX); return 0; }')
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(tmp_path / "m")],
+                   check=True)
+    most = int(subprocess.run([str(tmp_path / "m")], capture_output=True, text=True, check=True).stdout)
+    import gated_delta_rule_65_amd as pkg
+    assert most == P.PAGED_ATTENTION_WORKSPACE_MAX == pkg.PAGED_ATTENTION_WORKSPACE_MAX
+    seen = []
+    for dim in (64, 128):
+        for dtype in (0, 1):
+            for hq, hkv in ((1, 1), (32, 8), (64, 1), (7, 7)):
+                for n in (1, 2, 4, 33, 256):
+                    for hint in (0, 1):
+                        for splits in (0, 2, 64):
+                            for k in range(18):
+                                seen.append(workspace(lib, total_tokens=n + (1 << k) - 1, n=n, hq=hq, hkv=hkv,
+                                                      head_dim=dim, dtype=dtype, max_pages=8192,
+                                                      num_pages=8192, max_new_len=hint, splits=splits))
+    assert (1 << 30) * 3 // 4 < max(seen) <= most and min(seen) == 0
+
+
+def test_the_columns_in_use_bound_the_workspace(lib):
+    """A narrow view of a wide table asks for less."""
+    sizes = [workspace(lib, splits=0, n=4, hq=32, hkv=8, total_tokens=1024, max_pages=m, table_stride=8192)
+             for m in (1, 16, 64, 256, 8192)]
+    assert sizes == sorted(sizes) and sizes[0] == 0 and sizes[3] < sizes[4] // 4
+    q, kc = torch.zeros(1024, 32, 128, dtype=torch.bfloat16), torch.zeros(1, 8, 16, 128, dtype=torch.bfloat16)
+    table = torch.zeros(4, 8192, dtype=torch.int32)
+    assert [P.paged_attention_workspace_bytes(q, kc, kc, table[:, :m]) for m in (16, 256, 8192)] == \
+        [sizes[1], sizes[3], sizes[4]]
+
+
 def cpu_case(dt=torch.bfloat16):
     q = torch.zeros(3, 4, 128, dtype=dt)
     kc = torch.zeros(5, 2, 16, 128, dtype=dt)

@@ -250,6 +250,17 @@ def test_a_workspace_of_the_queried_size_with_host_offsets(asked):
     check(c, 16, (out.cpu(), lse.cpu()))
 
 
+def test_one_workspace_for_steps_of_all_sizes():
+    """Steps that need more bytes the smaller they are, in the workspace that serves any."""
+    ws = torch.empty(paged.PAGED_ATTENTION_WORKSPACE_MAX, dtype=torch.uint8, device=DEV)
+    needs = []
+    for new in ([2500, 9, 600, 1], [200, 9, 160, 1], [1, 1, 1, 1]):
+        c = R.make([700, 40, 0, 1500], new, 64, 64, 64, 16, BF, seed=15, pad_rows=2, extra_cols=1200)
+        needs.append(paged.paged_attention_workspace_bytes(c.q, c.k_cache, c.v_cache, c.table))
+        check_rows(c, 16, attend(c, 16, workspace=ws), 0, 0)
+    assert needs[0] == 0 and needs[1] > needs[2] > 0
+
+
 def test_many_requests_and_heads_that_are_no_power_of_two():
     """More requests than one look at the offsets covers, in both kernels."""
     ctx = [(37 * i) % 60 for i in range(150)]
