@@ -105,9 +105,9 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
   if (a->max_new_len < 0) FAIL(KDA_ERR_SHAPE, "max_new_len must be >= 0");
   if (a->splits < 0 || a->splits > MAX_SPLITS)
     FAIL(KDA_ERR_SHAPE, "splits must lie in [0, %d], got %d", MAX_SPLITS, a->splits);
-  // hidden scores are -inf before the scale
-  if (!isfinite(a->scale) || a->scale <= 0.0f)
-    FAIL(KDA_ERR_SHAPE, "scale must be finite and above 0");
+  // hidden scores are -inf before the scale, which the kernels take times log2(e)
+  if (!isfinite(a->scale * 1.4426950408889634f) || a->scale <= 0.0f)
+    FAIL(KDA_ERR_SHAPE, "scale must be above 0 and finite in base two (below 2.35e38)");
   if ((int64_t)a->max_pages * a->page_size > MAX_KEYS)
     FAIL(KDA_ERR_UNSUPPORTED, "max_pages * page_size above 2^30");
   if ((int64_t)a->hq * a->head_dim > MAX_STRIDE)

@@ -130,7 +130,9 @@ kda_status kda_kv_append(const kda_kv_append_args *a);
  * Scores, softmax statistics and sums are held in fp32; for 16-bit types the
  * probabilities are rounded to the input type for their product with V, and out
  * is rounded once.  A row that sees no key (a position below 0, no page) gets
- * zeros and lse = -inf, as does one whose scores are all -inf.  What lies at
+ * zeros and lse = -inf, as does one whose scores are all -inf.  Scaled scores stay
+ * below 2.35e38 (fp32's largest over log2(e)), values below 2^119 over the number of
+ * keys (they are summed with weights of up to 2^8 before the division).  What lies at
  * positions that a row does not see does not reach it, be it infinite or NaN.
  * Rows of out and lse behind the last request are left as they are.  A length
  * beyond the table's width reads the table's positions only.
@@ -168,7 +170,7 @@ typedef struct kda_paged_attention_args {
                                   0 = unknown; results do not depend on it, but
                                   for the order of sums */
   int32_t splits;              /* 0 = auto, else at most that many (1..64) */
-  float scale;                 /* finite and > 0 (head_dim^-0.5 is the usual value) */
+  float scale;                 /* > 0 and below 2.35e38 (head_dim^-0.5 is the usual value) */
   void *stream;                /* hipStream_t or NULL */
 } kda_paged_attention_args;
 

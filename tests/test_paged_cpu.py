@@ -185,6 +185,14 @@ def test_workspace_follows_the_splits(lib):
     assert workspace(lib, splits=0, max_pages=1 << 16, total_tokens=2) > 0
 
 
+def test_scales_that_overflow_in_base_two_are_refused(lib):
+    """The kernels' exponents are in base two: scale * log2(e) has to be finite."""
+    n = ctypes.c_size_t(0)
+    for scale, status in ((2.35e38, B.KDA_OK), (2.4e38, SHAPE), (3.4e38, SHAPE)):
+        assert lib.kda_paged_attention_workspace_size(ctypes.byref(attend(scale=scale)),
+                                                      ctypes.byref(n)) == status
+
+
 def test_one_workspace_serves_every_shape(lib, tmp_path):
     src = tmp_path / "m.c"
     src.write_text('#include <stdio.h>\n#include "kda_paged.h"\n'
