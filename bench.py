@@ -171,15 +171,20 @@ class HipEvents:
 
 # ------------------------------------------------------------------- helpers
 
-# The paged attention sources, which none of these workloads runs.
-NOT_KDA = ("kda_attn", "kda_page_tables", "kda_paged")
+# The paged attention kernels and their C ABI, which none of these workloads runs and no
+# other source includes.
+NOT_KDA = ("kda_attn", "kda_page_tables", "kda_paged_api")
+
+
+def kda_sources():
+    """The files under csrc/ that the workloads' kernels and launch plans are built from."""
+    return [p for p in sorted(glob.glob(os.path.join(ROOT, "gated_delta_rule_65_amd", "csrc", "*")))
+            if not os.path.basename(p).startswith(NOT_KDA)]
 
 
 def source_hash():
     h = hashlib.sha256()
-    for p in sorted(glob.glob(os.path.join(ROOT, "gated_delta_rule_65_amd", "csrc", "*"))):
-        if os.path.basename(p).startswith(NOT_KDA):
-            continue
+    for p in kda_sources():
         with open(p, "rb") as f:
             h.update(os.path.basename(p).encode())
             h.update(f.read())

@@ -9,6 +9,8 @@ diagonal), the unit-lower inverse (a triangular solve, L^3 / 3), and w and u
 qg S and kg^T U (64 x 128 x 128 each), A_qk U (lower) and scales the state by
 its decay.  Byte counts are the tensors each kernel must read or write once.
 """
+import os
+import re
 import subprocess
 import sys
 
@@ -88,3 +90,13 @@ def test_more_than_one_gpu_is_refused(n):
                        capture_output=True, text=True, timeout=60)
     assert r.returncode == 2
     assert "one GPU only" in r.stdout + r.stderr
+
+
+def test_source_hash_covers_what_its_sources_include():
+    """Counters are dropped once a file changes that the kernels they were taken of, or
+    the plans of their launches, are built from."""
+    hashed = {os.path.basename(p) for p in bench.kda_sources()}
+    assert {"kda_chunk.hip", "kda_decode.hip", "kda_verify.hip", "kda_onchip.hip", "kda_api.hip"} <= hashed
+    for p in bench.kda_sources():
+        for name in re.findall(r'#include "([^"]+)"', open(p).read()):
+            assert os.path.basename(name) in hashed or name.startswith("../../include/"), (p, name)
