@@ -7,11 +7,13 @@
 //
 // Bound by the matrix cores where chunks are long: a tile costs a wave 128 products (4096
 // cycles for 128 channels), a SIMD holds two waves, and the ring keeps three tiles on
-// their way.  2048 tokens on 8192 keys, 8 heads on 2, 128 channels: 560 us, 107 TFLOP/s, where
-// a large library product reaches 154; with the keys split over the waves, each of which
-// then reads every row tile's keys from L2 by itself, 690 us.  Products first and V reads
-// three ahead of them brought 576 us to 560; two tiles a barrier change nothing.  Short
-// chunks are bound by the start of a workgroup (the rows kernel has those below 256 rows).
+// their way.  2048 tokens on 8192 keys, 8 heads on 2, 128 channels: 540 to 560 us a call, 112
+// to 107 TFLOP/s (507 to 514 of them this kernel, 23 the join), where a large library
+// product reaches 154; with the keys split over the waves, each of which then reads every
+// row tile's keys from L2 by itself, 690 us.  Products first and V reads three ahead of
+// them brought 576 us to 560; two tiles a barrier change nothing.  Short chunks leave the
+// matrix cores idle: 840 tokens take 34 us at 20 % (the rows kernel has those below 256
+// rows).
 #include "kda_attn.hpp"
 
 namespace kda {

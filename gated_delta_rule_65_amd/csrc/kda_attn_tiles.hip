@@ -11,8 +11,9 @@
 // beside 32 exponentials (nearly as much), and a SIMD holds two waves (256 registers).
 // So the two have to be out of step, one multiplying while the other weighs.  They
 // drift apart by themselves where barriers are rare; products go first (s_setprio).
-// 2048 tokens on 131072 keys, 32 heads on 8, takes 3.7 ms (1.17 PFLOP/s, matrix cores
-// 56 % busy; a large library product reaches 1.23).  Measured on the way, same case:
+// 2048 tokens on 131072 keys, 32 heads on 8, takes 3.7 to 3.95 ms from card to card (1.18
+// to 1.10 PFLOP/s, matrix cores 55 % busy; a large library product reaches 1.23).  Measured
+// on the way, same case, one card:
 //   a barrier a tile, both waves in step                          4.26 ms
 //   the phases of the two waves held apart by barriers            4.46 ms
 //   a tile's products woven into the softmax of the one before    4.60 ms

@@ -11,7 +11,8 @@
 // token 3.9 us, 1000 requests with 93766 tokens 5.6 us.
 //
 // Append.  A copy of 16-byte pieces, bound by HBM: 32768 tokens of 8 heads of 128 fp16
-// channels (134 MB read, 134 MB written) 53 us, 5.0 TB/s; a large copy reaches 4.8.
+// channels (134 MB read, 134 MB written) 53 us, 5.0 TB/s; a large copy reaches 4.8.  (42 us
+// where the last-level cache still holds the same rows from the call before.)
 #include "kda_common.hpp"
 #include "kda_paged.hpp"
 

@@ -172,7 +172,11 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
     L.min_keys = units + (int64_t)a->n * a->hkv >= 2048 ? 2048 : units >= 256 ? 1024 : 512;
     grid = units >= (L.tile_waves == 8 ? 256 : 512) * (a->n > 1 ? 3 : 1) ? 0 : units >= 256 ? 8192 : 1024;
   } else {
-    // (chunks: with 32, 64, 96 and 128 keys at least the 840 tokens take 46, 40, 43 and 51 us)
+    // chunks: 64 keys at least.  With 32, 64, 96, 128 and 256 keys 3 chunks of 840 tokens take
+    // 51, 41, 48, 58 and 75 us, 300 tokens on 700 keys 27, 24, 31, 34 and 63 us, 4 fresh
+    // ones of 512 tokens 67, 55, 53, 66 and 88 us; longer visits would like more: 8 of
+    // 256 tokens on 1000 (64 channels) 77, 77, 70, 74 and 75 us, 2 of 400 tokens on 3000
+    // 136, 133, 120, 106 and 92 us.
     units = L.by_request ? (int64_t)a->n * a->hkv
                          : ceil_div(group_rows, L.chunks ? kda::CHUNK_ROWS : 16 * L.row_blocks) * a->hkv;
     L.min_keys = units >= 1024 ? 2048 : units >= 256 ? 1024 : L.chunks ? 64 : 256;
