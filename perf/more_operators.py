@@ -1,0 +1,614 @@
+"""Rotary positions and a paged cache in 8 bits: plain forms, and the cases they are measured on.
+
+The attention layers of a hybrid model, from the projection to the output, with a
+cache of half the bytes:
+
+* ``rotary``   the step's query and key rows turned to their positions (or back, which
+               is the gradient), both pair layouts, part of the head, scaled frequencies;
+* ``append``   the step's key and value rows into the cache, 8 bits a value and one
+               scale per block of tokens and head, then the blocks it touched read back;
+* ``read``     the cached rows of requests read back;
+* ``attend``   attention of the new tokens over the cache, causal, with an optional
+               sliding window and first tokens that stay visible.
+
+A scale is a power of two: the least one with which the block's largest magnitude is
+a code (448 for e4m3, 127 for int8).  A block that already has rows keeps its scale or
+takes a larger one, and its rows are then rounded to it.  The cache is ``[pages, kv
+heads, page size, head dim]``, the scales ``[pages, kv heads, blocks per page]``.
+``run`` computes the plain form where ``own`` is false and calls the package's entry
+points where it is true.
+"""
+import math
+
+import torch
+
+
+own = False
+
+_DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+_MOST = {"e4m3": 448.0, "int8": 127.0}
+_DEV = "cuda"
+
+
+# --------------------------------------------------------------------- cases
+
+def listed():
+    return [
+        # one decode step of a full batch, rows out of the fused projection
+        dict(name="rotary decode", op="rotary", tokens=256, hq=32, hkv=8, dim=128, rot=128,
+             inter=False, inverse=False, far=8192, stretch=1.0, fused=True, dtype="bf16"),
+        # a prefill step, part of the head, frequencies stretched for a long context
+        dict(name="rotary prefill", op="rotary", tokens=32768, hq=32, hkv=8, dim=128, rot=64,
+             inter=True, inverse=False, far=1 << 20, stretch=16.0, fused=False, dtype="fp16"),
+        # the gradient's turn back, full precision, a count that is not round
+        dict(name="rotary back", op="rotary", tokens=4099, hq=16, hkv=16, dim=64, rot=64,
+             inter=False, inverse=True, far=5000, stretch=1.0, fused=False, dtype="fp32"),
+        # one decode step's rows of a full batch: latency, some blocks' scales grow
+        dict(name="append decode", op="append", n=256, lo=0, hi=200, new_lo=1, new_hi=1, hkv=8,
+             dim=128, page=16, block=16, code="e4m3", dtype="bf16"),
+        # a prefill step's rows: fresh and continued prompts of ragged lengths
+        dict(name="append prefill", op="append", n=24, lo=0, hi=700, new_lo=64, new_hi=5000,
+             hkv=8, dim=128, page=64, block=32, code="int8", dtype="bf16"),
+        # the contexts of a batch, handed on in 16 bits
+        dict(name="read batch", op="read", n=24, lo=64, hi=8192, hkv=8, dim=128, page=48,
+             block=16, code="e4m3", dtype="bf16"),
+        # a few short contexts at full precision, as for a check
+        dict(name="read few", op="read", n=5, lo=1, hi=300, hkv=4, dim=64, page=20, block=5,
+             code="int8", dtype="fp32"),
+        # decode of a full batch with lengths spread as in the varlen workload
+        dict(name="decode batch", op="attend", n=256, lo=64, hi=8192, new_lo=1, new_hi=1,
+             hq=32, hkv=8, dim=128, page=16, block=16, window=0, sinks=0, code="e4m3",
+             dtype="bf16"),
+        # decode of one request far into a long context: latency
+        dict(name="decode long", op="attend", n=1, lo=131072, hi=131072, new_lo=1, new_hi=1,
+             hq=32, hkv=8, dim=128, page=64, block=64, window=0, sinks=0, code="int8",
+             dtype="bf16"),
+        # decode in windowed layers, 64-wide heads, contexts far past the window
+        dict(name="decode window", op="attend", n=64, lo=1000, hi=100000, new_lo=1, new_hi=1,
+             hq=16, hkv=16, dim=64, page=32, block=16, window=2047, sinks=4, code="e4m3",
+             dtype="fp16"),
+        # the last chunk of a very long prompt
+        dict(name="chunk long", op="attend", n=1, lo=129024, hi=129024, new_lo=2048, new_hi=2048,
+             hq=32, hkv=8, dim=128, page=64, block=64, window=0, sinks=0, code="e4m3",
+             dtype="bf16"),
+        # a mixed step: chunks of a few prompts beside short drafts, pages of an odd size
+        dict(name="mixed step", op="attend", n=33, lo=1, hi=6000, new_lo=1, new_hi=700,
+             hq=24, hkv=8, dim=64, page=48, block=24, window=0, sinks=0, code="int8",
+             dtype="bf16"),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["rotary", "rotary", "append", "append", "read", "attend", "attend", "attend"])
+    hq, hkv = rng.choice([(32, 8), (16, 16), (24, 8), (8, 1), (32, 4), (6, 2), (5, 1)])
+    dim = rng.choice([64, 128, 128])
+    dtype = rng.choice(["bf16", "bf16", "fp16", "fp32"])
+    if op == "rotary":
+        return dict(op=op, tokens=_log_int(rng, 1, 16384), hq=hq, hkv=hkv, dim=dim,
+                    rot=rng.choice([dim, dim, dim // 2, dim // 4, 2 * rng.randint(1, dim // 2)]),
+                    inter=rng.random() < 0.5, inverse=rng.random() < 0.3,
+                    far=_log_int(rng, 16, 1 << 24), stretch=rng.choice([1.0, 4.0, 40.0]),
+                    fused=rng.random() < 0.5, dtype=dtype)
+    page, block = rng.choice([(8, 8), (16, 16), (16, 4), (32, 16), (48, 24), (64, 64), (64, 16),
+                              (128, 128), (20, 5), (20, 20), (16, 1)])
+    code = rng.choice(["e4m3", "e4m3", "int8"])
+    paged = dict(op=op, hkv=hkv, dim=dim, page=page, block=block, code=code)
+    if op == "append":
+        n = _log_int(rng, 1, 256)
+        new = rng.choice([1, 1, 4, _log_int(rng, 1, max(1, 16384 // n))])
+        return dict(paged, n=n, lo=0, hi=_log_int(rng, 1, 1000), new_lo=max(1, new // 3),
+                    new_hi=new, dtype=dtype)
+    if op == "read":
+        n = _log_int(rng, 1, 64)
+        hi = _log_int(rng, 1, 32768 // n)
+        return dict(paged, n=n, lo=max(1, hi // rng.choice([1, 3, 50])), hi=hi, dtype=dtype)
+    dtype = rng.choice(["bf16", "bf16", "fp16"])
+    windowed = rng.random() < 0.4
+    window = _log_int(rng, 16, 4096) if windowed else 0
+    sinks = rng.choice([0, 1, 4, 16, 70]) if windowed else 0
+    attend = dict(paged, hq=hq, window=window, sinks=sinks, dtype=dtype)
+    if rng.random() < 0.5:       # decode, of a token or a short draft each
+        n = _log_int(rng, 1, 256)
+        new = rng.choice([1, 1, 1, 4])
+        ctx = _log_int(rng, 16, min(131072, 1 << 20 >> max(0, n.bit_length() - 1)))
+        return dict(attend, n=n, lo=max(1, ctx // rng.choice([1, 4, 64])), hi=ctx, new_lo=new,
+                    new_hi=new)
+    n = _log_int(rng, 1, 24)     # chunks
+    new = _log_int(rng, 2, 4096)
+    ctx = rng.choice([0, _log_int(rng, 1, 16384)])
+    while n > 1 and 4.0 * n * new * (ctx + new) * hq * dim > 4e12:
+        n -= 1
+    return dict(attend, n=n, lo=ctx // 2, hi=ctx, new_lo=max(1, new // rng.choice([1, 3, 50])),
+                new_hi=new)
+
+
+# -------------------------------------------------------------------- inputs
+
+def _spread(case, lo, hi, salt):
+    """Whole numbers spread over the logarithm of lo .. hi.  They belong to the case, not to
+    the seed, so that a pass costs the same on every seed."""
+    g = torch.Generator().manual_seed(salt + case["n"])
+    u = torch.rand(case["n"], generator=g, dtype=torch.float64)
+    a, b = math.log(lo + 1), math.log(hi + 1)
+    return torch.clamp(torch.round(torch.exp(a + u * (b - a)) - 1), lo, hi).to(torch.int64)
+
+
+def _lengths(case):
+    """(cached, new) lengths of the case's requests."""
+    ctx = _spread(case, case["lo"], case["hi"], 1000)
+    ctx[0] = case["hi"]
+    if case["op"] == "read":
+        return ctx.tolist(), ctx.tolist()
+    new = _spread(case, case["new_lo"], case["new_hi"], 2000)
+    new[-1] = case["new_hi"]     # the longest one is there
+    return ctx.tolist(), new.tolist()
+
+
+def _generator(seed):
+    return torch.Generator(device=_DEV).manual_seed(seed)
+
+
+def _i32(values):
+    return torch.tensor(values, dtype=torch.int32, device=_DEV)
+
+
+def _starts(lens):
+    out = [0]
+    for t in lens:
+        out.append(out[-1] + t)
+    return out
+
+
+def _pages(n, page):
+    return -(-n // page)
+
+
+def _bits(codes):
+    """Codes as bytes: torch moves those of every type."""
+    return codes.view(torch.uint8)
+
+
+def _least_scale(top, code):
+    """The least power of two with which magnitudes up to `top` (fp32) are codes."""
+    frac, exp = torch.frexp(top)
+    edge, bits = (0.875, 9) if code == "e4m3" else (0.9921875, 7)
+    e = torch.where(frac > edge, exp - bits + 1, exp - bits).clamp(min=-126)
+    return torch.where(top > 0, torch.ldexp(torch.ones_like(top), e), 2.0 ** -126)
+
+
+def _encode(y, code):
+    """fp32 values within the codes' range, rounded to codes."""
+    if code == "e4m3":
+        return y.to(torch.float8_e4m3fn)
+    return torch.round(y).to(torch.int8)
+
+
+def _cache(case, pages, g):
+    """(codes, scales) of rows whose sizes differ from block to block and channel to channel."""
+    hkv, dim, page, block = case["hkv"], case["dim"], case["page"], case["block"]
+    shape = (pages, hkv, page // block, block, dim)
+    x = torch.randn(shape, generator=g, device=_DEV)
+    x *= torch.exp(0.3 * torch.randn(shape[:3] + (1, 1), generator=g, device=_DEV))
+    x *= torch.exp(0.3 * torch.randn((1, hkv, 1, 1, dim), generator=g, device=_DEV))
+    s = _least_scale(x.abs().amax((3, 4)), case["code"])
+    codes = _encode(x / s[..., None, None], case["code"])
+    return codes.view(pages, hkv, page, dim), s
+
+
+def _table(used, g, cols):
+    """A block table of shuffled pages, and the pages of the cache."""
+    num_pages = sum(used) + 2
+    host = torch.randperm(num_pages, generator=g, device=_DEV).to(torch.int32).cpu()
+    table = torch.full((len(used), cols), -1, dtype=torch.int32)
+    at = 0
+    for i, u in enumerate(used):
+        table[i, :u] = host[at:at + u]
+        at += u
+    return table.to(_DEV), num_pages
+
+
+def _frequencies(case):
+    """[rot / 2] radians per position (fp64); stretched ones are slowed by that factor
+    where the stretched context has less than a turn, not where it has 32, and between."""
+    rot = case["rot"]
+    i = torch.arange(rot // 2, dtype=torch.float64, device=_DEV)
+    f = torch.pow(torch.tensor(10000.0, dtype=torch.float64, device=_DEV), -2 * i / rot)
+    if case["stretch"] > 1.0:
+        turns = case["far"] / case["stretch"] * f / (2 * math.pi)
+        keep = ((turns - 1) / 31).clamp(0, 1)
+        f = f * keep + f / case["stretch"] * (1 - keep)
+    return f
+
+
+def prepare(case, seed):
+    g = _generator(seed)
+    hkv, dim, dt = case["hkv"], case["dim"], _DT[case["dtype"]]
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device=_DEV, dtype=torch.float32).to(dt)
+
+    if case["op"] == "rotary":
+        tokens, hq = case["tokens"], case["hq"]
+        if case["fused"]:
+            proj = normal(tokens, hq + 2 * hkv, dim)
+            q, k = proj[:, :hq], proj[:, hq:hq + hkv]
+        else:
+            q, k = normal(tokens, hq, dim), normal(tokens, hkv, dim)
+        pos = torch.randint(0, case["far"], (tokens,), generator=g, device=_DEV)
+        return dict(case=case, q=q, k=k, positions=pos.to(torch.int32),
+                    frequencies=_frequencies(case),
+                    scale=1.0 if case["stretch"] == 1.0 else 0.1 * math.log(case["stretch"]) + 1.0)
+    page, block = case["page"], case["block"]
+    ctx, new = _lengths(case)
+    total = list(ctx) if case["op"] == "read" else [c + t for c, t in zip(ctx, new)]
+    used = [_pages(t, page) for t in total]
+    table, num_pages = _table(used, g, max(used) + 2)
+    kc, ks = _cache(case, num_pages, g)
+    vc, vs = _cache(case, num_pages, g)
+    s = dict(case=case, k_cache=kc, v_cache=vc, k_scale=ks, v_scale=vs, table=table,
+             cu=_i32(_starts(new)), seq_lens=_i32(total), page=page, block=block,
+             code=case["code"], dtype=dt)
+    if case["op"] == "read":
+        s["tokens"] = sum(new)
+    elif case["op"] == "append":
+        # rows of the fused projection, now and then a large one
+        proj = torch.randn(sum(new), 2, hkv, dim, generator=g, device=_DEV)
+        proj *= torch.exp(0.5 * torch.randn(sum(new), 2, hkv, 1, generator=g, device=_DEV))
+        proj = proj.to(dt)
+        back = [t - c // block * block for c, t in zip(ctx, total)]    # rows of touched blocks
+        s |= dict(k=proj[:, 0], v=proj[:, 1], back_cu=_i32(_starts(back)), back=sum(back))
+    else:
+        s |= dict(q=normal(sum(new), case["hq"], dim), max_new=max(new), new_host=new,
+                  total_host=total, scale=dim ** -0.5, window=case["window"], sinks=case["sinks"])
+    return s
+
+
+# --------------------------------------------------------------- plain forms
+
+def _rotary_plain(s):
+    case, n = s["case"], s["frequencies"].numel()
+    angle = s["positions"].double()[:, None] * s["frequencies"]
+    if case["inverse"]:
+        angle = -angle
+    cos = (s["scale"] * torch.cos(angle)).float()[:, None]
+    sin = (s["scale"] * torch.sin(angle)).float()[:, None]
+
+    def turn(t):
+        x = t[..., :2 * n].float()
+        a, b = (x[..., 0::2], x[..., 1::2]) if case["inter"] else (x[..., :n], x[..., n:])
+        u, w = a * cos - b * sin, a * sin + b * cos
+        x = torch.stack([u, w], -1).flatten(-2) if case["inter"] else torch.cat([u, w], -1)
+        return torch.cat([x.to(t.dtype), t[..., 2 * n:]], -1)
+
+    return dict(q=turn(s["q"]), k=turn(s["k"]))
+
+
+def _places(s, cu, tokens):
+    """(request, position, page id) of the rows of cu."""
+    cu, seq = cu.long(), s["seq_lens"].long()
+    t = torch.arange(tokens, device=_DEV)
+    req = torch.searchsorted(cu[1:].contiguous(), t, right=True)
+    pos = seq[req] - cu[req + 1] + t
+    return req, pos, s["table"][req, pos // s["page"]].long()
+
+
+def _append_plain(s):
+    page, block, code = s["page"], s["block"], s["code"]
+    per = page // block
+    req, pos, at = _places(s, s["cu"], s["k"].shape[0])
+    off = pos % page
+    blk = at * per + off // block                       # the row's block among all
+    pages, hkv = s["k_scale"].shape[:2]
+    first = torch.full((pages * per,), block, device=_DEV)
+    first.scatter_reduce_(0, blk, off % block, "amin")  # the block's first new row
+    touched = first < block
+    row = torch.arange(page, device=_DEV)
+    for x, cache, scale in ((s["k"], s["k_cache"], s["k_scale"]), (s["v"], s["v_cache"], s["v_scale"])):
+        x = x.float()
+        top = torch.zeros(pages * per, hkv, device=_DEV)
+        top.index_reduce_(0, blk, x.abs().amax(-1), "amax")
+        old = scale.permute(0, 2, 1).reshape(pages * per, hkv)
+        new = torch.maximum(_least_scale(top, code), torch.where((first > 0)[:, None], old, 0.0))
+        new = torch.where(touched[:, None], new, old)
+        # the rows of grown blocks that came before, rounded to the larger scale
+        shrink = torch.where((touched & (first > 0))[:, None], old / new, 1.0)
+        shrink = shrink.view(pages, per, hkv).permute(0, 2, 1)[:, :, row // block]
+        before = row % block < first.view(pages, per)[:, row // block]
+        shrink = torch.where(before[:, None], shrink, 1.0)
+        cache.copy_(_encode(cache.float() * shrink[..., None], code))
+        scale.copy_(new.view(pages, per, hkv).permute(0, 2, 1))
+        _bits(cache)[at, :, off] = _bits(_encode(x / new[blk][..., None], code))
+    k, v = _read_plain(s, s["back_cu"], s["back"], torch.float32)
+    return dict(k=k, v=v, k_scale=s["k_scale"], v_scale=s["v_scale"])
+
+
+def _values(cache, scale, pages, off, block):
+    """fp32 values of the rows at (pages, off)."""
+    codes = _bits(cache)[pages, :, off].view(cache.dtype)
+    return codes.float() * scale[pages, :, off // block][..., None]
+
+
+def _read_plain(s, cu, tokens, dtype):
+    req, pos, at = _places(s, cu, tokens)
+    off = pos % s["page"]
+    return (_values(s["k_cache"], s["k_scale"], at, off, s["block"]).to(dtype),
+            _values(s["v_cache"], s["v_scale"], at, off, s["block"]).to(dtype))
+
+
+def _attend_block(s, reqs, q, qpos, kpos):
+    """q [B, R, Hq, D] at positions qpos [B, R], over the positions kpos [B, L]
+    of the requests' pages; -1 is no key."""
+    hkv, page = s["k_cache"].shape[1], s["page"]
+    b, r, hq, d = q.shape
+    at = s["table"][reqs[:, None], kpos.clamp(min=0) // page].long()
+    off = kpos.clamp(min=0) % page
+    k = _values(s["k_cache"], s["k_scale"], at, off, s["block"]).permute(0, 2, 3, 1).contiguous()
+    v = _values(s["v_cache"], s["v_scale"], at, off, s["block"]).permute(0, 2, 1, 3).contiguous()
+    qf = q.float().view(b, r, hkv, hq // hkv, d).permute(0, 2, 3, 1, 4)
+    qf = qf.reshape(b, hkv, (hq // hkv) * r, d)
+    gap = qpos[:, :, None] - kpos[:, None, :]
+    seen = (gap >= 0) & (kpos >= 0)[:, None, :]
+    if s["window"]:
+        seen &= (gap < s["window"]) | (kpos < s["sinks"])[:, None, :]
+    x = torch.matmul(qf, k).view(b, hkv, hq // hkv, r, -1)
+    x = torch.where(seen[:, None, None], x * s["scale"], -math.inf)
+    top = x.amax(-1, keepdim=True)
+    top = torch.where(top == -math.inf, 0.0, top)
+    p = torch.exp(x - top)
+    total = p.sum(-1, keepdim=True)
+    o = torch.matmul(p.view(b, hkv, -1, p.shape[-1]), v).view(b, hkv, hq // hkv, r, d)
+    o = torch.where(total > 0, o / total, 0.0)
+    lse = (top + torch.log(total)).squeeze(-1)
+    return (o.permute(0, 3, 1, 2, 4).reshape(b, r, hq, d), lse.permute(0, 3, 1, 2).reshape(b, r, hq))
+
+
+def _key_positions(s, first, last):
+    """The positions that queries at first .. last see at all."""
+    lo = max(0, first - s["window"] + 1) if s["window"] else 0
+    return torch.cat([torch.arange(min(s["sinks"], lo), device=_DEV),
+                      torch.arange(lo, last + 1, device=_DEV)])
+
+
+def _attend_plain(s):
+    q, hq = s["q"], s["q"].shape[1]
+    new, total = s["new_host"], s["total_host"]
+    out = torch.empty_like(q)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=_DEV)
+    if max(new) == min(new) and max(new) <= 4:      # decode: all requests at once
+        n, r = len(new), new[0]
+        qpos = s["seq_lens"].long()[:, None] - r + torch.arange(r, device=_DEV)[None, :]
+        if s["window"]:
+            lo = (qpos[:, :1] - s["window"] + 1).clamp(min=0)
+            kpos = lo + torch.arange(s["window"] + r - 1, device=_DEV)[None, :]
+            kpos = torch.where(kpos <= qpos[:, -1:], kpos, -1)
+            first = torch.arange(s["sinks"], device=_DEV)[None, :].expand(n, -1)
+            kpos = torch.cat([torch.where(first < lo, first, -1), kpos], 1)
+        else:
+            kpos = torch.arange(max(total), device=_DEV)[None, :].expand(n, -1)
+            kpos = torch.where(kpos <= qpos[:, -1:], kpos, -1)
+        o, e = _attend_block(s, torch.arange(n, device=_DEV), q.view(n, r, hq, -1), qpos, kpos)
+        out.copy_(o.reshape(out.shape))
+        lse.copy_(e.reshape(lse.shape))
+        return dict(out=out, lse=lse)
+    # chunks: request by request, in blocks whose scores fit comfortably
+    at = 0
+    for i, (t, length) in enumerate(zip(new, total)):
+        wide = min(length, s["window"] + s["sinks"] + 1024) if s["window"] else length
+        step = max(1, min(t, 1024 if s["window"] else t, (1 << 29) // (hq * wide)))
+        for b in range(0, t, step):
+            e = min(t, b + step)
+            p0, p1 = length - t + b, length - t + e - 1
+            qpos = torch.arange(p0, p1 + 1, device=_DEV)[None, :]
+            o, z = _attend_block(s, torch.full((1,), i, device=_DEV), q[None, at + b:at + e],
+                                 qpos, _key_positions(s, p0, p1)[None, :])
+            out[at + b:at + e] = o[0]
+            lse[at + b:at + e] = z[0]
+        at += t
+    return dict(out=out, lse=lse)
+
+
+def run(state):
+    op = state["case"]["op"]
+    if own:
+        from gated_delta_rule_65_amd import paged_q8, rotary
+        if op == "rotary":
+            case = state["case"]
+            q, k = rotary.rotary(state["q"], state["k"], state["positions"], state["frequencies"],
+                                 interleaved=case["inter"], scale=state["scale"],
+                                 inverse=case["inverse"])
+            return dict(q=q, k=k)
+        cache = (state["k_cache"], state["v_cache"], state["k_scale"], state["v_scale"])
+        table, seq = state["table"], state["seq_lens"]
+        if op == "append":
+            paged_q8.kv_append_q8(state["k"], state["v"], *cache, table, state["cu"], seq)
+            k, v = paged_q8.kv_read_q8(*cache, table, state["back_cu"], seq,
+                                       total_tokens=state["back"], dtype=torch.float32)
+            return dict(k=k, v=v, k_scale=state["k_scale"], v_scale=state["v_scale"])
+        if op == "read":
+            k, v = paged_q8.kv_read_q8(*cache, table, state["cu"], seq,
+                                       total_tokens=state["tokens"], dtype=state["dtype"])
+            return dict(k=k, v=v)
+        out, lse = paged_q8.paged_attention_q8(
+            state["q"], *cache, table, state["cu"], seq, scale=state["scale"],
+            window=state["window"], sinks=state["sinks"], return_lse=True,
+            max_new_len=state["max_new"])
+        return dict(out=out, lse=lse)
+    if op == "rotary":
+        return _rotary_plain(state)
+    if op == "append":
+        return _append_plain(state)
+    if op == "read":
+        k, v = _read_plain(state, state["cu"], state["tokens"], state["dtype"])
+        return dict(k=k, v=v)
+    return _attend_plain(state)
+
+
+# --------------------------------------------------------------- work, exact
+
+def _visible(pos, window, sinks):
+    """Keys that a query at position pos sees."""
+    if not window or pos + 1 <= window:
+        return pos + 1
+    return window + min(sinks, pos + 1 - window)
+
+
+def _sum_visible(first, last, window, sinks):
+    """The sum of _visible over positions first .. last."""
+    if not window:
+        return (first + last + 2) * (last - first + 1) // 2
+    edge = min(last + 1, max(first, window + sinks))
+    head = sum(_visible(p, window, sinks) for p in range(first, edge))
+    return head + (last + 1 - edge) * (window + sinks)
+
+
+def work(case):
+    hkv, dim = case["hkv"], case["dim"]
+    es = 4 if case["dtype"] == "fp32" else 2
+    if case["op"] == "rotary":
+        rows = case["tokens"] * (case["hq"] + hkv)
+        return dict(bytes=2 * rows * dim * es + 4 * case["tokens"] + 4 * case["rot"],
+                    flops=3 * rows * case["rot"])
+    ctx, new = _lengths(case)
+    row, block = hkv * dim, case["block"]
+    if case["op"] == "read":
+        # codes, their scales and the table in; rows out
+        tokens = sum(new)
+        return dict(bytes=2 * tokens * row * (1 + es) + 8 * hkv * (tokens // block + case["n"])
+                    + 4 * (tokens // case["page"] + 2 * case["n"]), flops=2 * tokens * row)
+    if case["op"] == "append":
+        # rows in, codes and scales out; the touched blocks read back as fp32
+        back = sum(c + t - c // block * block for c, t in zip(ctx, new))
+        scales = sum(_pages(c + t, block) - c // block for c, t in zip(ctx, new))
+        return dict(bytes=2 * sum(new) * row * (es + 1) + 2 * back * row * (1 + 4)
+                    + 24 * hkv * scales + 16 * case["n"], flops=4 * sum(new) * row)
+    w, sinks = case["window"], case["sinks"]
+    keys = pairs = 0
+    for c, t in zip(ctx, new):
+        pairs += _sum_visible(c, c + t - 1, w, sinks)
+        lo = max(0, c - w + 1) if w else 0
+        keys += c + t - lo + min(sinks if w else 0, lo)
+    tokens = sum(new)
+    return dict(bytes=2 * keys * row + 8 * hkv * (keys // block) + 4 * (keys // case["page"])
+                + tokens * case["hq"] * (2 * dim * es + 4) + 8 * case["n"],
+                flops=4 * pairs * case["hq"] * dim)
+
+
+def _code_64(y, code):
+    """fp64 values rounded to the nearest code's value, ties to even."""
+    if code == "int8":
+        return torch.round(y)
+    step = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
+    return torch.round(y / step) * step
+
+
+def _scale_64(top, code):
+    """The least power of two s >= 2^-126 with top <= largest code * s."""
+    e = -126
+    if top > 0:
+        e = max(e, math.ceil(math.log2(top / _MOST[code])) - 2)
+        while math.ldexp(_MOST[code], e) < top:
+            e += 1
+    return math.ldexp(1.0, e)
+
+
+def _exact_append(case, s):
+    """Request by request and block by block, in fp64."""
+    block, page, hkv = case["block"], case["page"], case["hkv"]
+    ctx, new = _lengths(case)
+    if case["n"] * hkv * (_pages(max(new), block) + 1) > 60000:
+        return None
+    got, table = {}, s["table"].cpu()
+    for name in ("k", "v"):
+        x = s[name].double().cpu()
+        scale = s[name + "_scale"].cpu().clone()
+        codes = s[name + "_cache"].float().cpu()
+        rows, at = [], 0
+        for c, t in zip(ctx, new):
+            i = len(rows)
+            parts = []
+            for b in range(c // block, _pages(c + t, block)):
+                lo, hi = max(c, b * block), min(c + t, (b + 1) * block)
+                pg, o = int(table[i, b * block // page]), b * block % page
+                fresh = x[at + lo - c:at + hi - c]                          # [rows, hkv, dim]
+                tops = fresh.abs().amax((0, 2)).tolist()
+                need = torch.tensor([_scale_64(z, case["code"]) for z in tops], dtype=torch.float64)
+                old = scale[pg, :, o // block].double()
+                sc = need if lo == b * block else torch.maximum(old, need)
+                held = codes[pg, :, o:o + lo - b * block].double().permute(1, 0, 2)
+                held = _code_64(held * (old / sc)[None, :, None], case["code"])
+                fresh = _code_64(fresh / sc[None, :, None], case["code"])
+                parts.append(torch.cat([held, fresh]) * sc[None, :, None])
+                scale[pg, :, o // block] = sc.float()
+            rows.append(torch.cat(parts))
+            at += t
+        got[name] = torch.cat(rows)
+        got[name + "_scale"] = scale.double()
+    return got
+
+
+def _rows_64(s, name, i, length):
+    """[length, hkv, dim] values of request i, page by page in fp64."""
+    cache, scale = s[name + "_cache"], s[name + "_scale"]
+    pages = s["table"][i, :_pages(length, s["page"])].long()
+    x = _bits(cache)[pages].view(cache.dtype).double()
+    x = x * torch.repeat_interleave(scale[pages].double(), s["block"], 2)[..., None]
+    return x.permute(0, 2, 1, 3).reshape(-1, cache.shape[1], cache.shape[3])[:length]
+
+
+def exact(case, seed):
+    """The definitions in 64 bits: pairs as complex numbers, blocks one by one, every key of a
+    request against every query, the invisible ones taken out of the softmax."""
+    s = prepare(case, seed)
+    if case["op"] == "rotary":
+        n = s["frequencies"].numel()
+        angle = s["positions"].double()[:, None] * s["frequencies"] * (-1 if case["inverse"] else 1)
+        wheel = torch.polar(torch.full_like(angle, s["scale"]), angle)[:, None]
+        got = {}
+        for name in ("q", "k"):
+            x = s[name].double().clone()
+            if case["inter"]:
+                z = torch.view_as_complex(x[..., :2 * n].reshape(x.shape[:2] + (n, 2)).contiguous())
+                x[..., :2 * n] = torch.view_as_real(z * wheel).flatten(-2)
+            else:
+                z = torch.complex(x[..., :n].contiguous(), x[..., n:2 * n].contiguous()) * wheel
+                x[..., :n], x[..., n:2 * n] = z.real, z.imag
+            got[name] = x
+        return got
+    if case["op"] == "append":
+        return _exact_append(case, s)
+    ctx, new = _lengths(case)
+    if case["op"] == "read":
+        return {name: torch.cat([_rows_64(s, name, i, c) for i, c in enumerate(ctx)])
+                for name in ("k", "v")}
+    hq, hkv, dim = case["hq"], case["hkv"], case["dim"]
+    group = hq // hkv
+    out = torch.zeros(s["q"].shape, dtype=torch.float64, device=_DEV)
+    lse = torch.zeros(s["q"].shape[:2], dtype=torch.float64, device=_DEV)
+    start = 0
+    for i in range(case["n"]):
+        length = ctx[i] + new[i]
+        keys, values = _rows_64(s, "k", i, length), _rows_64(s, "v", i, length)
+        j = torch.arange(length, device=_DEV)
+        for h in range(hkv):
+            kt, v = keys[:, h].t().contiguous(), values[:, h].contiguous()
+            step = max(1, (1 << 27) // (group * length))
+            for b in range(0, new[i], step):
+                rows = min(step, new[i] - b)
+                sl = slice(start + b, start + b + rows)
+                heads = slice(h * group, (h + 1) * group)
+                pos = ctx[i] + b + torch.arange(rows, device=_DEV)
+                hidden = j[None] > pos[:, None]
+                if case["window"]:
+                    old = j[None] <= pos[:, None] - case["window"]
+                    hidden |= old & (j[None] >= case["sinks"])
+                x = s["q"][sl, heads].double().reshape(rows * group, dim) @ kt * dim ** -0.5
+                x = x.view(rows, group, length).masked_fill(hidden[:, None], -math.inf)
+                lse[sl, heads] = torch.logsumexp(x, -1)
+                w = torch.softmax(x, -1).view(rows * group, length)
+                out[sl, heads] = (w @ v).view(rows, group, dim)
+        start += new[i]
+    return dict(out=out, lse=lse)
