@@ -414,12 +414,12 @@ def _attend_plain(s):
 def run(state):
     op = state["case"]["op"]
     if own:
-        from gated_delta_rule_65_amd import paged_q8, rotary
+        from gated_delta_rule_65_amd import paged_q8, positions
         if op == "rotary":
             case = state["case"]
-            q, k = rotary.rotary(state["q"], state["k"], state["positions"], state["frequencies"],
-                                 interleaved=case["inter"], scale=state["scale"],
-                                 inverse=case["inverse"])
+            q, k = positions.rotary(state["q"], state["k"], state["positions"],
+                                    state["frequencies"], interleaved=case["inter"],
+                                    scale=state["scale"], inverse=case["inverse"])
             return dict(q=q, k=k)
         cache = (state["k_cache"], state["v_cache"], state["k_scale"], state["v_scale"])
         table, seq = state["table"], state["seq_lens"]
