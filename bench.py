@@ -171,9 +171,9 @@ class HipEvents:
 
 # ------------------------------------------------------------------- helpers
 
-# The paged attention kernels and their C ABI, which none of these workloads runs and no
-# other source includes.
-NOT_KDA = ("kda_attn", "kda_page_tables", "kda_paged_api")
+# The rotary and paged attention kernels and their C ABI, which none of these workloads runs
+# and no other source includes.
+NOT_KDA = ("kda_attn", "kda_page_tables", "kda_paged_api", "kda_rotary")
 
 
 def kda_sources():
