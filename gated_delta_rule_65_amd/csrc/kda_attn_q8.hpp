@@ -120,19 +120,60 @@ __device__ __forceinline__ float inverse_scale(float s) {
   return __uint_as_float((254u << 23) - __float_as_uint(s));
 }
 
-// The last request i, of n, whose first item (by `first`, which grows with i) is at most
-// `item`.  All lanes of a wave ask together; 64 requests a round.
-template <typename F> __device__ __forceinline__ int find_request(int n, int item, int lane, F first) {
+// A request's rows: the first, their number, and its length.
+struct Rows {
+  int req, start, len, seq;
+};
+// The last request whose first item (by `first` of its index and first row, which grows with the index)
+// is at most `item`; all lanes of a wave ask together.  Up to 256 requests are looked through
+// in one round trip to memory, offsets and lengths at once; more take one per factor of 64.
+template <typename F>
+__device__ __forceinline__ Rows find_rows(const int32_t* cu, const int32_t* seq, int n, int total, int item,
+                                          int lane, F first) {
+  Rows r;
+  auto clamp = [&](int c) { return min(max(c, 0), total); };
+  if (n <= 256) {
+    constexpr int M = 4;
+    int c[M], s[M];
+    const int last = clamp(cu[n]);
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      c[j] = s[j] = 0;
+      if (64 * j < n) {
+        const int i = min(64 * j + lane, n - 1);
+        c[j] = clamp(cu[i]);
+        s[j] = seq[i];
+      }
+    }
+    r.req = -1;
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const int i = 64 * j + lane;
+      r.req += __popcll(__ballot(i == 0 || (i < n && first(i, c[j]) <= item)));
+    }
+    auto at = [&](const int (&v)[M], int i) {
+      const int x = i < 64 ? v[0] : i < 128 ? v[1] : i < 192 ? v[2] : v[3];
+      return __builtin_amdgcn_readlane(x, i & 63);
+    };
+    r.start = at(c, r.req);
+    r.len = max(r.req + 1 < n ? at(c, r.req + 1) : last, r.start) - r.start;
+    r.seq = max(at(s, r.req), 0);
+    return r;
+  }
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int step = (hi - lo + 63) / 64;
     const int i = lo + lane * step;
-    const bool in = lane == 0 || (i < hi && first(i) <= item);
+    const bool in = lane == 0 || (i < hi && first(i, clamp(cu[i])) <= item);
     const int k = __popcll(__ballot(in)) - 1;
     lo += k * step;
     hi = min(hi, lo + step);
   }
-  return lo;
+  r.req = lo;
+  r.start = clamp(cu[lo]);
+  r.len = max(clamp(cu[lo + 1]), r.start) - r.start;
+  r.seq = max(seq[lo], 0);
+  return r;
 }
 
 }  // namespace kda

@@ -70,12 +70,11 @@ __global__ __launch_bounds__(256) void append_q8_kernel(const CacheQ8Launch a, u
   if (w >= units) return;
   const uint32_t item = fdiv(w, a.hdiv);
   const int head = (int)(w - item * a.hkv);
-  auto start_of = [&](int i) { return min(max(a.cu[i], 0), a.total); };
-  const int req = find_request(a.n, (int)item, lane,
-                               [&](int i) { return (int)fdiv(start_of(i), a.block) + 2 * i; });
-  const int start = start_of(req), len = min(max(a.cu[req + 1], start), a.total) - start;
-  const int64_t seq = max(a.seq[req], 0), pos0 = seq - len;
-  const int local = (int)item - ((int)fdiv(start, a.block) + 2 * req);
+  auto first_item = [&](int i, int start) { return (int)fdiv(start, a.block) + 2 * i; };
+  const Rows own = find_rows(a.cu, a.seq, a.n, a.total, (int)item, lane, first_item);
+  const int req = own.req, start = own.start, len = own.len;
+  const int64_t seq = own.seq, pos0 = seq - len;
+  const int local = (int)item - first_item(req, start);
   if (local < 0) return;  // offsets that decrease
   // the block, among those of the request, and its new rows
   const int B = (int)a.block.d;
@@ -84,14 +83,7 @@ __global__ __launch_bounds__(256) void append_q8_kernel(const CacheQ8Launch a, u
   if (lo >= hi) return;
   const int page_at = (int)fdiv((uint32_t)at, a.page);  // at < capacity
   const int id = a.table[(int64_t)req * a.table_stride + page_at];
-  if ((uint32_t)id >= (uint32_t)a.num_pages) return;
-  const int off = (int)at - page_at * (int)a.page.d;  // of the block in its page
   const int rows = (int)(hi - lo), held = (int)(lo - at);
-  const int64_t row_at = ((int64_t)head * a.page.d + off) * DIM;
-  uint8_t* const kc = (uint8_t*)a.kc + id * a.k_page + row_at;
-  uint8_t* const vc = (uint8_t*)a.vc + id * a.v_page + row_at;
-  const int64_t sc = ((int64_t)id * a.hkv + head) * a.per_page + fdiv(off, a.block);
-  const float ks0 = held > 0 ? a.ks[sc] : 0.0f, vs0 = held > 0 ? a.vs[sc] : 0.0f;
 
   const int first = (WAVES == 1 ? 0 : wave * (64 / LPR)) + lane / LPR, col = 8 * (lane % LPR);
   const int64_t x0 = start + (lo - pos0);
@@ -108,9 +100,17 @@ __global__ __launch_bounds__(256) void append_q8_kernel(const CacheQ8Launch a, u
       }
     }
   };
+  load(0);  // beside the table's entry, which only the codes' place needs
+  if ((uint32_t)id >= (uint32_t)a.num_pages) return;
+  const int off = (int)at - page_at * (int)a.page.d;  // of the block in its page
+  const int64_t row_at = ((int64_t)head * a.page.d + off) * DIM;
+  uint8_t* const kc = (uint8_t*)a.kc + id * a.k_page + row_at;
+  uint8_t* const vc = (uint8_t*)a.vc + id * a.v_page + row_at;
+  const int64_t sc = ((int64_t)id * a.hkv + head) * a.per_page + fdiv(off, a.block);
+  const float ks0 = held > 0 ? a.ks[sc] : 0.0f, vs0 = held > 0 ? a.vs[sc] : 0.0f;
   float ktop = 0.0f, vtop = 0.0f;
   for (int r0 = 0; r0 < rows; r0 += HOLD * RPL) {
-    load(r0);
+    if (r0 > 0) load(r0);
 #pragma unroll
     for (int i = 0; i < HOLD; ++i)
       if (r0 + i * RPL + first < rows) {
@@ -171,9 +171,22 @@ __global__ __launch_bounds__(256) void append_q8_kernel(const CacheQ8Launch a, u
 
 constexpr int READ_ROWS = 16;
 
-template <typename E> __device__ __forceinline__ void store8(E* p, const float (&x)[8]) {
-  store4(p, x[0], x[1], x[2], x[3]);
-  store4(p + 4, x[4], x[5], x[6], x[7]);
+template <typename E, int CODE> __device__ __forceinline__ void store_scaled(E* p, uint2 u, float s) {
+  float x[4], y[4];
+  Code<CODE>::widen(u.x, x);
+  Code<CODE>::widen(u.y, y);
+  if constexpr (sizeof(E) == 4) {
+    store4(p, x[0] * s, x[1] * s, x[2] * s, x[3] * s);
+    store4(p + 4, y[0] * s, y[1] * s, y[2] * s, y[3] * s);
+  } else {
+    typename Half<E>::frag f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      Half<E>::set(f, i, x[i] * s);
+      Half<E>::set(f, 4 + i, y[i] * s);
+    }
+    *reinterpret_cast<typename Half<E>::frag*>(p) = f;
+  }
 }
 
 template <typename E, int DIM, int CODE>
@@ -182,14 +195,14 @@ __global__ __launch_bounds__(256) void read_q8_kernel(const CacheQ8Launch a, Fas
   __shared__ int64_t s_k[READ_ROWS], s_v[READ_ROWS], s_s[READ_ROWS];  // bytes, bytes, scales; -1: no page
   const int tid = threadIdx.x, lane = tid & 63;
   const int item = (int)blockIdx.x;
-  auto start_of = [&](int i) { return min(max(a.cu[i], 0), a.total); };
-  const int req = find_request(a.n, item, lane, [&](int i) { return start_of(i) / READ_ROWS + i; });
-  const int start = start_of(req), len = min(max(a.cu[req + 1], start), a.total) - start;
+  const Rows own = find_rows(a.cu, a.seq, a.n, a.total, item, lane,
+                             [&](int i, int start) { return start / READ_ROWS + i; });
+  const int req = own.req, start = own.start, len = own.len;
   const int first = (item - (start / READ_ROWS + req)) * READ_ROWS;
   if (first < 0 || first >= len) return;
   const int rows = min(READ_ROWS, len - first);
   if (tid < rows) {
-    const int64_t pos = (int64_t)max(a.seq[req], 0) - len + first + tid;
+    const int64_t pos = (int64_t)own.seq - len + first + tid;
     int64_t kb = -1, vb = -1, sb = 0;
     if (pos >= 0 && pos < a.capacity) {
       const int pg = (int)fdiv((uint32_t)pos, a.page), off = (int)pos - pg * (int)a.page.d;
@@ -204,28 +217,37 @@ __global__ __launch_bounds__(256) void read_q8_kernel(const CacheQ8Launch a, Fas
   }
   __syncthreads();
   const int64_t head = (int64_t)a.page.d * DIM;  // bytes between heads
-  for (uint32_t x = tid; x < rows * per_token.d; x += 256) {
-    const uint32_t t = fdiv(x, per_token), p = x - t * per_token.d;
-    const int h = (int)(p / LPR), col = 8 * (int)(p % LPR);
-    const int64_t kb = s_k[t];
-    float y[8] = {}, z[8] = {};
-    if (kb >= 0) {
-      const uint2 ku = *(const uint2*)((const uint8_t*)a.kc + kb + h * head + col);
-      const uint2 vu = *(const uint2*)((const uint8_t*)a.vc + s_v[t] + h * head + col);
-      const float ks = a.ks[s_s[t] + (int64_t)h * a.per_page], vs = a.vs[s_s[t] + (int64_t)h * a.per_page];
-      float c[4], d[4];
-      Code<CODE>::widen(ku.x, c);
-      Code<CODE>::widen(ku.y, d);
+  const uint32_t total = rows * per_token.d;
+  // AT_ONCE steps' loads go out together: a few rows are bound by latency
+  constexpr int AT_ONCE = 4;
+  for (uint32_t x0 = tid; x0 < total; x0 += 256 * AT_ONCE) {
+    uint2 ku[AT_ONCE], vu[AT_ONCE];
+    float ks[AT_ONCE], vs[AT_ONCE];
+    int64_t to[AT_ONCE];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = c[i] * ks, y[4 + i] = d[i] * ks;
-      Code<CODE>::widen(vu.x, c);
-      Code<CODE>::widen(vu.y, d);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] = c[i] * vs, z[4 + i] = d[i] * vs;
+    for (int j = 0; j < AT_ONCE; ++j) {
+      const uint32_t x = x0 + 256 * j;
+      ku[j] = vu[j] = make_uint2(0, 0);
+      ks[j] = vs[j] = 0.0f;
+      if (x < total) {
+        const uint32_t t = fdiv(x, per_token), p = x - t * per_token.d;
+        const int h = (int)(p / LPR), col = 8 * (int)(p % LPR);
+        to[j] = (int64_t)(start + first + (int)t) * a.hkv * DIM + 8 * (int64_t)p;
+        const int64_t kb = s_k[t];
+        if (kb >= 0) {
+          ku[j] = *(const uint2*)((const uint8_t*)a.kc + kb + h * head + col);
+          vu[j] = *(const uint2*)((const uint8_t*)a.vc + s_v[t] + h * head + col);
+          ks[j] = a.ks[s_s[t] + (int64_t)h * a.per_page];
+          vs[j] = a.vs[s_s[t] + (int64_t)h * a.per_page];
+        }
+      }
     }
-    const int64_t at = (int64_t)(start + first + (int)t) * a.hkv * DIM + h * DIM + col;
-    store8((E*)a.ko + at, y);
-    store8((E*)a.vo + at, z);
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {
+      if (x0 + 256 * j >= total) break;
+      store_scaled<E, CODE>((E*)a.ko + to[j], ku[j], ks[j]);
+      store_scaled<E, CODE>((E*)a.vo + to[j], vu[j], vs[j]);
+    }
   }
 }
 

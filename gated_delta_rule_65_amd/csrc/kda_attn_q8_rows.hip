@@ -43,25 +43,34 @@ __device__ __forceinline__ u32x2v_t lds_read_tr8(uint32_t at) {
       (__attribute__((address_space(3))) i32x2_t*)(uintptr_t)at));
 }
 
+// A NaN code of V spoils the product of its tile also for rows that do not see its key (0 times
+// NaN).  Where a sum is not finite, the keys are gone through twice more: once with NaN codes
+// as ones and the others as zeros, each visible key weighing one, which finds the sums that a NaN
+// belongs to, and once with zeros for NaN.
+enum { PLAIN = 0, COUNT = 1, ZEROED = 2 };
+__device__ __forceinline__ uint32_t without_nan(uint32_t w, int mode) {
+  const uint32_t nan = (((w & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u) * 0xffu;  // bytes 0x7f, 0xff
+  return mode == COUNT ? nan & 0x38383838u : w & ~nan;                                   // (0x38 is 1)
+}
+
 struct Tile {
   int base;        // its first key
   uint32_t valid;  // which of its keys exist
 };
 
 template <typename E, int DIM, int RB, int CODE>
-__global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
+__global__ __launch_bounds__(256, RB == 1 ? 4 : 2) void rows_q8_kernel(const AttnQ8Launch a) {
   typedef typename Half<E>::frag frag;
   constexpr uint32_t ALL = ~0u;
   constexpr bool PAIR = std::is_same_v<E, _Float16>;  // probabilities as a pair of bf16
   constexpr int P = DIM / 16;                    // 16-byte pieces per row
   constexpr int NI = KT * P / 64;                // DMA instructions per K or V tile
   constexpr int QS = DIM / 32;                   // fragments of a row
-  constexpr int STAGE = 2 * KT * P + 16;         // pieces of a K and a V tile and their scales
+  constexpr int STAGE = 2 * KT * P + 32;         // pieces of a K and a V tile, and two tiles' scales
   constexpr int ROWS = 64 / P, ROW = DIM;        // keys of a DMA instruction, bytes of one
-  constexpr int DMAS = 2 * NI + 1;
   constexpr int OS = DIM + 4;                    // floats per joined row (padded)
   constexpr int JOIN = WAVES * 16 * RB * OS / 4;
-  constexpr int PIECES = WAVES * 2 * STAGE > JOIN ? WAVES * 2 * STAGE : JOIN;
+  constexpr int PIECES = WAVES * STAGE > JOIN ? WAVES * STAGE : JOIN;
   __shared__ __attribute__((aligned(1024))) uint4 smem[PIECES];
   __shared__ float sm_m[WAVES][16 * RB], sm_l[WAVES][16 * RB];
 
@@ -74,7 +83,7 @@ __global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
   if (rt.rows == 0) return;
   const int seq = rt.seq, pos0 = seq - rt.len;
   const float c = a.scale * LOG2E;
-  uint4* const my = smem + wave * 2 * STAGE;
+  uint4* const my = smem + wave * STAGE;
   // this lane's piece of an instruction's keys, as bytes from the first of them
   const uint32_t koff = lane / P * ROW + 16 * (lane % P ^ kswz<P>(lane / P));
   const uint32_t voff = lane / P * ROW + 16 * (lane % P ^ vswz<P>(lane / P));
@@ -84,12 +93,11 @@ __global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
   const uint32_t ka = lds_addr(my + l16 * P + (gq ^ kswz<P>(l16)));
   const int vrow = 4 * gq + ((l16 >> 1) & 3) + 16 * (l16 >> 3);
   const uint32_t va = lds_addr(my + KT * P + vrow * P + vswz<P>(vrow)) + 8 * (l16 & 1);
-  const uint32_t sa = lds_addr(my + 2 * KT * P);  // scales of K, then of V
+  const uint32_t sa = lds_addr(my + 2 * KT * P);  // scales of K, then of V; 256 bytes on, the other tile's
   const bool even = a.page.d % ROWS == 0;         // whether an instruction's keys share a page
   PageWindow pages(a, rt.req);
   const char* const kbase = (const char*)a.kc + (int64_t)kvh * a.page.d * ROW;
   const char* const vbase = (const char*)a.vc + (int64_t)kvh * a.page.d * ROW;
-  const float* const scales = (lane < KT ? a.scales.k : a.scales.v) + (int64_t)kvh * a.scales.per_page;
   const int64_t scale_page = (int64_t)a.hkv * a.scales.per_page;
 
   // One tile of rows, and the further ones of a request that has more than its hint said.
@@ -107,9 +115,11 @@ __global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
     // row, in the order of the keys' channels, and their positions
     u32x4v_t q[RB][QS];
     int qpos[RB];
+    int ql = lane;
+    asm volatile("" : "+v"(ql));  // or what follows would be kept through the walk
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
-      const int r = 16 * b + l16;
+      const int r = 16 * b + (ql & 15), gq = ql >> 4;
       const int tok = (int)fdiv(first + r, a.gdiv);
       const int head = kvh * a.group + first + r - tok * a.group;
       qpos[b] = pos0 + tok;
@@ -139,28 +149,33 @@ __global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
       }
       return t;
     };
-    // Issues the DMA of its codes and scales.
-    auto issue = [&](const Tile& t, int stage) __attribute__((always_inline)) {
-      uint4* const kt = my + stage * STAGE;
-      uint4* const vt = kt + KT * P;
-      {  // lane l: K's scale of key l % 32, or V's
-        const int r = lane & (KT - 1), key = t.base + r, pg = (int)fdiv(key, a.page);
-        const int64_t page = pages.at(pg);
-        const float* p = scales + page * scale_page + fdiv(key - pg * (int)a.page.d, a.scales.block);
-        if (!((t.valid >> r) & 1)) p = (const float*)&attn_zero;
-        dma4(p, lds_addr(kt + 2 * KT * P));
-      }
+    // Issues the DMA of its K codes and of its scales, or of its V codes.
+    auto issue_scales = [&](const Tile& t, int slot) __attribute__((always_inline)) {
+      // lane l: K's scale of key l % 32, or V's
+      int ln = lane;
+      asm volatile("" : "+v"(ln));  // or the pool's address would be kept
+      const float* const scales = (ln < KT ? a.scales.k : a.scales.v) + (int64_t)kvh * a.scales.per_page;
+      const int r = ln & (KT - 1), key = t.base + r, pg = (int)fdiv(key, a.page);
+      const int64_t page = pages.at(pg);
+      const float* p = scales + page * scale_page + fdiv(key - pg * (int)a.page.d, a.scales.block);
+      if (!((t.valid >> r) & 1)) p = (const float*)&attn_zero;
+      dma4(p, lds_addr(my + 2 * KT * P + 16 * slot));
+    };
+    auto issue = [&](const Tile& t, bool v) __attribute__((always_inline)) {
+      uint4* const to = v ? my + KT * P : my;
+      const char* const pool = v ? vbase : kbase;
+      const int64_t stride = v ? a.v_page : a.k_page;
       if (even && t.valid == ALL) {
         // one page per instruction: the addresses are scalar work
-        uint32_t ko = koff, vo = voff;
-        asm volatile("" : "+v"(ko), "+v"(vo));  // or every x would keep its registers
+        uint32_t o = v ? voff : koff;
+        asm volatile("" : "+v"(o));  // or every x would keep its register
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
           const int key = t.base + x * ROWS, pg = (int)fdiv(key, a.page);
           const int64_t off = key - pg * (int)a.page.d, page = pages.uniform_at(pg);
           // (the swizzles are linear: that of row r0 + x ROWS is r0's xor that of x ROWS)
-          dma16(kbase + page * a.k_page + off * ROW, ko ^ 16 * kswz<P>(x * ROWS), lds_addr(kt + 64 * x));
-          dma16(vbase + page * a.v_page + off * ROW, vo ^ 16 * vswz<P>(x * ROWS), lds_addr(vt + 64 * x));
+          dma16(pool + page * stride + off * ROW, o ^ 16 * (v ? vswz<P>(x * ROWS) : kswz<P>(x * ROWS)),
+                lds_addr(to + 64 * x));
         }
         return;
       }
@@ -169,52 +184,19 @@ __global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
         const int r = (64 * x + lane) / P, ps = lane % P, key = t.base + r;
         const int pg = (int)fdiv(key, a.page);
         const int64_t off = key - pg * (int)a.page.d, page = pages.at(pg);
-        const char* kp = kbase + page * a.k_page + off * ROW + 16 * (ps ^ kswz<P>(r));
-        const char* vp = vbase + page * a.v_page + off * ROW + 16 * (ps ^ vswz<P>(r));
-        if (!((t.valid >> r) & 1)) kp = vp = (const char*)&attn_zero;
-        dma16(kp, lds_addr(kt + 64 * x));
-        dma16(vp, lds_addr(vt + 64 * x));
+        const char* p = pool + page * stride + off * ROW + 16 * (ps ^ (v ? vswz<P>(r) : kswz<P>(r)));
+        if (!((t.valid >> r) & 1)) p = (const char*)&attn_zero;
+        dma16(p, lds_addr(to + 64 * x));
       }
     };
 
-    // O += P V key by key on the vector unit, added where the key is visible: e4m3 V may hold
-    // NaN that some rows must not see (0 times it is NaN).  s: probabilities times scales.
     f32x4_t s[2][RB];
-    auto by_key = [&](const Tile& t, const uint4* vt) {
-#pragma unroll 1
-      for (int j = 0; j < KT; ++j) {
-        float p[RB];
-        uint32_t see[RB];  // all ones where the row sees the key
-#pragma unroll
-        for (int b = 0; b < RB; ++b) {
-          float x = 0.0f;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) x = (j & 3) == r ? (j & 16 ? s[1][b][r] : s[0][b][r]) : x;
-          p[b] = __shfl(x, l16 + 16 * ((j >> 2) & 3));
-          see[b] = 0u - ((seen(a, t.base, qpos[b], t.valid) >> j) & 1);
-        }
-#pragma unroll
-        for (int d = 0; d < DIM / 16; ++d) {
-          __builtin_amdgcn_sched_barrier(0);  // few registers at a time
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(
-              reinterpret_cast<const char*>(vt + j * P + (d ^ vswz<P>(j))) + 4 * gq);
-          float v[4];
-          Code<CODE>::widen(w, v);
-#pragma unroll
-          for (int b = 0; b < RB; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              o[d][b][i] = fmaf(p[b], __uint_as_float(__float_as_uint(v[i]) & see[b]), o[d][b][i]);
-        }
-      }
-    };
-
-    auto scores = [&](int stage) __attribute__((always_inline)) {  // S^T = K Q^T
-      uint32_t at = ka + stage * (STAGE * 16);
+    auto scores = [&](int slot) __attribute__((always_inline)) {  // S^T = K Q^T
+      uint32_t at = ka;
       asm volatile("" : "+v"(at));  // or every step would keep its address
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float sk = lds_read4(sa + stage * (STAGE * 16) + 64 * k + 4 * l16);
+        const float sk = lds_read4(sa + 256 * slot + 64 * k + 4 * l16);
 #pragma unroll
         for (int b = 0; b < RB; ++b) s[k][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -231,10 +213,8 @@ __global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
         }
       }
     };
-    // The softmax of the tile's scores and its product with V.
-    // CAREFUL keeps the values of hidden keys out of the sums.
-    auto weigh = [&](auto careful, const Tile& t, int stage) __attribute__((always_inline)) {
-      constexpr bool CAREFUL = decltype(careful)::value;
+    // The softmax of the tile's scores, and its product with V once `values` says that it is there.
+    auto weigh = [&](int mode, const Tile& t, int slot, auto values) __attribute__((always_inline)) {
       // keys hidden from some rows, or absent
       const bool mixed = pa != pb && (t.base + KT - 1 > pa ||
                                       (a.window > 0 && t.base <= pb - a.window && t.base + KT > a.sinks));
@@ -276,7 +256,7 @@ __global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
         }
       }
       // the probabilities, times V's scales
-      const uint32_t sv = sa + stage * (STAGE * 16) + 4 * KT + 16 * gq;
+      const uint32_t sv = sa + 256 * slot + 4 * KT + 16 * gq;
       f32x4_t vs[2];
       vs[0] = __builtin_bit_cast(f32x4_t, lds_read16(sv));
       vs[1] = __builtin_bit_cast(f32x4_t, lds_read16(sv + 64));
@@ -308,10 +288,25 @@ __global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) s[k][b][r] *= vs[k][r];
       }
-      if constexpr (CAREFUL) {
-        if (mixed) {
-          by_key(t, my + stage * STAGE + KT * P);
-          return;
+      values();
+      if (CODE == E4M3 && mode != PLAIN) {
+#pragma unroll 1
+        for (int x = 0; x < NI; ++x) {
+          uint4* const at = my + KT * P + 64 * x + lane;
+          const uint4 u = *at;
+          *at = make_uint4(without_nan(u.x, mode), without_nan(u.y, mode), without_nan(u.z, mode),
+                           without_nan(u.w, mode));
+        }
+        lds_wait();
+      }
+      if (CODE == E4M3 && mode == COUNT) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          const uint32_t see = seen(a, t.base, qpos[b], t.valid) >> (4 * gq);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[k][b][r] = see & (1u << (16 * k + r)) ? 1.0f : 0.0f;
         }
       }
       // P^T as it lies: lane group gq holds keys 4 gq + r and 16 + 4 gq + r
@@ -324,10 +319,11 @@ __global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
           p[b][j] = (__bf16)x;
           if constexpr (PAIR) pl[b][j] = (__bf16)(x - (float)p[b][j]);
         }
-      uint32_t at = va + stage * (STAGE * 16);
+      uint32_t at = va;
       asm volatile("" : "+v"(at));
 #pragma unroll
       for (int d = 0; d < DIM / 16; ++d) {
+        if (d % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // few registers at a time
         const u32x2v_t w = lds_read_tr8(at ^ 16 * d);
         const u32x2v_t lo = Code<CODE>::widen16(bf16{}, w[0], 1.0f), hi = Code<CODE>::widen16(bf16{}, w[1], 1.0f);
         const bf16x8_t v = __builtin_bit_cast(bf16x8_t, u32x4v_t{lo[0], lo[1], hi[0], hi[1]});
@@ -342,7 +338,7 @@ __global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
     // contiguous tiles per wave
     const int share = (nt + WAVES - 1) / WAVES;
     const int w0 = t0 + min(nt, wave * share), w1 = t0 + min(nt, (wave + 1) * share);
-    auto walk = [&](auto careful) __attribute__((always_inline)) {
+    auto walk = [&](int mode) __attribute__((always_inline)) {
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
         m[b] = NEG_INF;
@@ -351,8 +347,11 @@ __global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
         for (int d = 0; d < DIM / 16; ++d) o[d][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
       if (w0 >= w1) return;
+      // one buffer each for K and V, refilled as soon as it is read
       Tile cur = locate(w0);
-      issue(cur, 0);
+      issue_scales(cur, 0);
+      issue(cur, false);
+      issue(cur, true);
       // the queries arrive here: a wait for them in the loop would wait for the DMA too
 #pragma unroll
       for (int b = 0; b < RB; ++b)
@@ -360,25 +359,32 @@ __global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
         for (int x = 0; x < QS; ++x) asm volatile("" : "+v"(q[b][x]));
 #pragma unroll 1
       for (int i = w0; i < w1; ++i) {
+        const bool more = i + 1 < w1;
+        const int slot = (i - w0) & 1;
         Tile next = cur;
-        const int stage = (i - w0) & 1;
-        if (i + 1 < w1) {
-          lds_wait();  // the reads of the tile that this one replaces
+        dma_wait<NI>();  // K and the scales of this tile; V may still be on its way
+        scores(slot);
+        lds_wait();
+        if (more) {
           next = locate(i + 1);
-          issue(next, stage ^ 1);
-          dma_wait<DMAS>();
-        } else {
-          dma_wait<0>();
+          issue_scales(next, slot ^ 1);
+          issue(next, false);
         }
-        scores(stage);
-        weigh(careful, cur, stage);
+        weigh(mode, cur, slot, [&] {
+          if (more) dma_wait<NI + 1>();
+          else dma_wait<0>();
+        });
+        lds_wait();
+        if (more) issue(next, true);
         cur = next;
       }
     };
-    walk(std::false_type{});
-    if constexpr (CODE == E4M3) {  // the code that has NaN
-      if (pa != pb) {  // else every key of a tile is visible to all rows
-        // a hidden NaN of V has spoilt the sums of its tile: once more, carefully
+    uint32_t nan_at[RB] = {};  // sums that a NaN belongs to, a bit each
+    for (int mode = PLAIN;;) {
+      walk(mode);
+      // int8 has no NaN, and with one position every key of a tile is visible to all rows
+      if (CODE != E4M3 || pa == pb || mode == ZEROED) break;
+      if (mode == PLAIN) {
         float z = 0.0f;  // becomes NaN if any sum is not finite
 #pragma unroll
         for (int b = 0; b < RB; ++b)
@@ -386,32 +392,55 @@ __global__ __launch_bounds__(256, 2) void rows_q8_kernel(const AttnQ8Launch a) {
           for (int d = 0; d < DIM / 16; ++d)
 #pragma unroll
             for (int r = 0; r < 4; ++r) z = fmaf(o[d][b][r], 0.0f, z);
-        if (__any(z != 0.0f)) {
-          lds_wait();
-          walk(std::true_type{});
-        }
+        if (!__any(z != 0.0f)) break;
+        mode = COUNT;
+      } else {
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int d = 0; d < DIM / 16; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              nan_at[b] |= o[d][b][r] > 0.0f ? 1u << (4 * d + r) : 0u;
+        mode = ZEROED;
       }
+      lds_wait();
+    }
+    if constexpr (CODE == E4M3) {
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+        if (__any(nan_at[b] != 0)) {
+#pragma unroll
+          for (int d = 0; d < DIM / 16; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (nan_at[b] >> (4 * d + r) & 1) o[d][b][r] = __builtin_nanf("");
+        }
     }
 
-    // join of the four waves
+    // join of the four waves (the thread's place worked out here, not kept through the walk)
+    int jl = lane;
+    asm volatile("" : "+v"(jl));
+    const int jq = jl >> 4, tid = jl + 64 * wave;
+    jl &= 15;
 #pragma unroll
     for (int b = 0; b < RB; ++b) l[b] = sum_quarter(l[b]);
     __syncthreads();
     float* const so = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
-      const int r = 16 * b + l16;
-      if (gq == 0) {
+      const int r = 16 * b + jl;
+      if (jq == 0) {
         sm_m[wave][r] = m[b];
         sm_l[wave][r] = l[b];
       }
 #pragma unroll
       for (int d = 0; d < DIM / 16; ++d)
-        *reinterpret_cast<f32x4_t*>(so + (wave * 16 * RB + r) * OS + 16 * d + 4 * gq) = o[d][b];
+        *reinterpret_cast<f32x4_t*>(so + (wave * 16 * RB + r) * OS + 16 * d + 4 * jq) = o[d][b];
     }
     __syncthreads();
     constexpr int PER = DIM / 4;  // threads per row
-    for (int x = threadIdx.x; x < rows * PER; x += 64 * WAVES) {
+    for (int x = tid; x < rows * PER; x += 64 * WAVES) {
       const int r = x / PER, d = 4 * (x % PER);
       float top = sm_m[0][r];
 #pragma unroll

@@ -19,6 +19,8 @@ from .paged import (_F, _I, _L, _P, _Z, _call, _fail, _int32, _on_gpu, _page_str
                     _same_device, _stream, _table)
 
 _CODES = {torch.float8_e4m3fn: 0, torch.int8: 1}
+_FP32, _BF16, _FP16 = torch.float32, torch.bfloat16, torch.float16
+_DENSE = torch.contiguous_format
 
 
 class KvAppendQ8Args(ctypes.Structure):
@@ -87,28 +89,37 @@ def load_library():
 
 def _codes(k_cache, v_cache, k_scale, v_scale):
     """(code, K page stride, V page stride, pages, Hkv, page size, D, block) of a cache."""
-    shape = k_cache.shape
+    shape, dtype = k_cache.shape, k_cache.dtype
     if len(shape) != 4:
         _fail("k_cache must be [pages, Hkv, page_size, D]")
     if v_cache.shape != shape:
         _fail("v_cache must have k_cache's shape")
-    code = _CODES.get(k_cache.dtype)
+    code = _CODES.get(dtype)
     if code is None:
-        _fail(f"k_cache must have dtype torch.float8_e4m3fn or torch.int8, got {k_cache.dtype}", TypeError)
-    if v_cache.dtype is not k_cache.dtype:
+        _fail(f"k_cache must have dtype torch.float8_e4m3fn or torch.int8, got {dtype}", TypeError)
+    if v_cache.dtype is not dtype:
         _fail("v_cache must have k_cache's dtype", TypeError)
     pages, hkv, page_size, dim = shape
     ss = k_scale.shape
-    if len(ss) != 3 or ss[0] != pages or ss[1] != hkv or ss[2] < 1 or page_size % ss[2]:
+    blocks = ss[2] if len(ss) == 3 and ss[0] == pages and ss[1] == hkv else 0
+    if blocks < 1 or page_size % blocks:
         _fail(f"k_scale must be [{pages}, {hkv}, blocks], blocks a divisor of page_size ({page_size})")
     if v_scale.shape != ss:
         _fail("v_scale must have k_scale's shape")
-    if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
+    if k_scale.dtype is not _FP32 or v_scale.dtype is not _FP32:
         _fail("k_scale and v_scale must have dtype torch.float32", TypeError)
     if not (k_scale.is_contiguous() and v_scale.is_contiguous()):
         _fail("k_scale and v_scale must be contiguous")
     return (code, _page_stride("k_cache", k_cache), _page_stride("v_cache", v_cache), pages, hkv,
-            page_size, dim, page_size // ss[2])
+            page_size, dim, page_size // blocks)
+
+
+def _one_device(dev, **tensors):
+    """As _same_device, for tensors that are all there: their indexes first, which cost less."""
+    on = -1 if dev.type == "cpu" else dev.index
+    for t in tensors.values():
+        if t.get_device() != on:
+            _same_device(dev, **tensors)
 
 
 def _requests(block_table, cu_seqlens, seq_lens, dev):
@@ -149,10 +160,8 @@ def kv_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqle
     dev = k.device
     n, cu, seq, stride, cols = _requests(block_table, cu_seqlens, seq_lens, dev)
     ks, vs = _rows_stride("k", k), _rows_stride("v", v)
-    if not (v.device == dev and k_cache.device == dev and v_cache.device == dev and
-            k_scale.device == dev and v_scale.device == dev and block_table.device == dev):
-        _same_device(dev, v=v, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-                     block_table=block_table)
+    _one_device(dev, v=v, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                block_table=block_table)
     _on_gpu(dev)
     lib = _lib or load_library()
     _call(lib.kda_kv_append_q8, KvAppendQ8Args(
@@ -190,17 +199,17 @@ def kv_read_q8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_
         _fail("total_tokens must be >= 0")
     n, cu, seq, stride, cols = _requests(block_table, cu_seqlens, seq_lens, dev)
     shape = (total_tokens, hkv, dim)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None:
-            _need(tuple(t.shape) == shape, f"{name} must have shape {list(shape)}")
+    if k_out is not None:
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            _need(t.shape == shape, f"{name} must have shape {list(shape)}")
             _need(t.dtype is dtype, f"{name} must have k_out's dtype", TypeError)
             _need(t.is_contiguous(), f"{name} must be contiguous")
-    _same_device(dev, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table,
-                 k_out=k_out, v_out=v_out)
+        _one_device(dev, k_out=k_out, v_out=v_out)
+    _one_device(dev, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table)
     _on_gpu(dev)
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=dev)
-        v_out = torch.empty(shape, dtype=dtype, device=dev)
+        v_out = torch.empty_like(k_out)
     lib = _lib or load_library()
     _call(lib.kda_kv_read_q8, KvReadQ8Args(
         _SIZEOF_READ, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
@@ -215,7 +224,7 @@ def _attention_args(q, k_cache, v_cache, k_scale, v_scale, block_table, n, scale
     shape, dtype = q.shape, q.dtype
     if len(shape) != 3:
         _fail("q must be [T, Hq, D]")
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+    if dtype is not _BF16 and dtype is not _FP16:
         _fail(f"q must have dtype torch.bfloat16 or torch.float16, got {dtype}", TypeError)
     T, hq, dim = shape
     code, kp, vp, pages, hkv, page_size, kdim, block = _codes(k_cache, v_cache, k_scale, v_scale)
@@ -289,11 +298,13 @@ def paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_se
         _need(lse.is_contiguous(), "lse must be contiguous")
     if workspace is not None:
         _need(workspace.is_contiguous(), "workspace must be contiguous")
-    _same_device(dev, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-                 block_table=block_table, output=output, lse=lse, workspace=workspace)
+    _one_device(dev, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                block_table=block_table)
+    if not (output is None and lse is None and workspace is None):
+        _same_device(dev, output=output, lse=lse, workspace=workspace)
     _on_gpu(dev)
     if output is None:
-        output = torch.empty(shape, dtype=q.dtype, device=dev)
+        output = torch.empty_like(q, memory_format=_DENSE)
     if return_lse and lse is None:
         lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
     lib = _lib or load_library()

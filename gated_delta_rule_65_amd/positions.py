@@ -31,6 +31,7 @@ class RotaryArgs(ctypes.Structure):
 
 
 _SIZEOF = ctypes.sizeof(RotaryArgs)
+_INT32, _FP64, _DENSE = torch.int32, torch.float64, torch.contiguous_format
 EXPORTS = ("kda_rotary",)
 _lib = None
 
@@ -94,23 +95,6 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
     return f if device is None else f.to(device)
 
 
-def _side(name, x, out, dev, dtype):
-    """(stride, out, its stride) of rows [T, H, D] and what they are turned into."""
-    if x.dtype is not dtype:
-        _fail(f"{name} must have dtype {dtype}", TypeError)
-    if x.device != dev:
-        _fail(f"{name} must be on {dev}")
-    stride = _rows_stride(name, x)
-    if out is None:
-        return stride, None, 0
-    if out is x:
-        return stride, x, stride
-    _need(out.shape == x.shape, f"{name}_out must have {name}'s shape")
-    _need(out.dtype is dtype, f"{name}_out must have {name}'s dtype", TypeError)
-    _need(out.device == dev, f"{name}_out must be on {dev}")
-    return stride, out, _rows_stride(name + "_out", out)
-
-
 def rotary(q, k, positions, frequencies, interleaved=False, scale=1.0, inverse=False, q_out=None,
            k_out=None):
     """Turns the rows of q [T, Hq, D] and k [T, Hk, D] (or None) to their positions
@@ -125,43 +109,69 @@ def rotary(q, k, positions, frequencies, interleaved=False, scale=1.0, inverse=F
     with respect to the outputs in their place.  bf16, fp16 or fp32, D a multiple of 8 up to
     512; q and k may be views of a fused projection.  q_out and k_out may be q and k themselves (in
     place) and otherwise share no memory with them."""
-    shape, dtype = q.shape, q.dtype
-    if len(shape) != 3:
+    if q.dim() != 3:
         _fail("q must be [T, Hq, D]")
-    if dtype not in _DTYPES:
+    T, hq, dim = q.shape
+    dtype = q.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
         _fail(f"unsupported dtype {dtype}", TypeError)
-    T, hq, dim = shape
-    dev = q.device
-    if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != dim):
-        _fail(f"k must be [{T}, Hk, {dim}]")
-    if k is None and k_out is not None:
-        _fail("k_out without k")
-    if positions.dim() != 1 or positions.shape[0] != T:
+    if positions.shape != (T,):
         _fail(f"positions must have shape [{T}]")
-    if positions.dtype is not torch.int32:
+    if positions.dtype is not _INT32:
         _fail("positions must have dtype torch.int32", TypeError)
-    if frequencies.dim() != 1 or not 1 <= frequencies.shape[0] <= dim // 2:
+    if frequencies.dim() != 1:
+        _fail("frequencies must be [n]")
+    n = frequencies.shape[0]
+    if not 1 <= n <= dim // 2:
         _fail(f"frequencies must be [n] with 1 <= n <= {dim // 2}")
-    if frequencies.dtype is not torch.float64:
+    if frequencies.dtype is not _FP64:
         _fail("frequencies must have dtype torch.float64", TypeError)
     if not (positions.is_contiguous() and frequencies.is_contiguous()):
         _fail("positions and frequencies must be contiguous")
-    if positions.device != dev or frequencies.device != dev:
-        _fail(f"positions and frequencies must be on {dev}")
-    qs, q_out, qos = _side("q", q, q_out, dev, dtype)
+    on = q.get_device()
+    if positions.get_device() != on or frequencies.get_device() != on:
+        _fail(f"positions and frequencies must be on {q.device}")
+    qs = _rows_stride("q", q)
     ks = kos = hk = 0
-    if k is not None:
+    if k is None:
+        if k_out is not None:
+            _fail("k_out without k")
+    else:
+        if k.dim() != 3 or k.shape[0] != T or k.shape[2] != dim:
+            _fail(f"k must be [{T}, Hk, {dim}]")
+        if k.dtype is not dtype:
+            _fail(f"k must have dtype {dtype}", TypeError)
+        if k.get_device() != on:
+            _fail(f"k must be on {q.device}")
         hk = k.shape[1]
-        ks, k_out, kos = _side("k", k, k_out, dev, dtype)
+        ks = _rows_stride("k", k)
+        if k_out is not None:
+            kos = _out_stride("k", k, k_out, ks)
+    qos = 0 if q_out is None else _out_stride("q", q, q_out, qs)
+    dev = q.device
     _on_gpu(dev)
     if q_out is None:
-        q_out = torch.empty(shape, dtype=dtype, device=dev)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=dtype, device=dev)
+        q_out = torch.empty_like(q, memory_format=_DENSE)
+    if k is None:
+        k_at = k_out_at = None
+    else:
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=_DENSE)
+        k_at, k_out_at = k.data_ptr(), k_out.data_ptr()
     lib = _lib or load_library()
     _call(lib.kda_rotary, RotaryArgs(
-        _SIZEOF, q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-        None if k is None else k_out.data_ptr(), positions.data_ptr(), frequencies.data_ptr(),
-        T, qs, ks, qos, kos, _DTYPES[dtype], hq, hk, dim, frequencies.shape[0],
-        bool(interleaved), bool(inverse), float(scale), _stream(dev)), dev)
+        _SIZEOF, q.data_ptr(), k_at, q_out.data_ptr(), k_out_at, positions.data_ptr(),
+        frequencies.data_ptr(), T, qs, ks, qos, kos, code, hq, hk, dim, n, bool(interleaved),
+        bool(inverse), float(scale), _stream(dev)), dev)
     return q_out, k_out
+
+
+def _out_stride(name, x, out, stride):
+    """Elements between the tokens of the rows that x is turned into."""
+    if out is x:
+        return stride
+    _need(out.shape == x.shape, f"{name}_out must have {name}'s shape")
+    _need(out.dtype is x.dtype, f"{name}_out must have {name}'s dtype", TypeError)
+    _need(out.device == x.device, f"{name}_out must be on {x.device}")
+    return _rows_stride(name + "_out", out)
