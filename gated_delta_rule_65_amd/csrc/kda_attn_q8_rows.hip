@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256, RB == 1 ? 4 : 2) void rows_q8_kernel(const Att
 
   const int lane = threadIdx.x & 63, wave = wave_of();
   const int l16 = lane & 15, gq = lane >> 4;
-  // heads fastest, so that neighbouring workgroups (and one XCD's) share pages
+  // heads fastest, so that neighbouring workgroups share pages
   const uint32_t unit = fdiv(blockIdx.x, a.hdiv);
   const int kvh = (int)(blockIdx.x - unit * a.hkv), split = blockIdx.y;
   const RowTile rt = request_tile(a, (int)unit);
@@ -321,11 +321,13 @@ __global__ __launch_bounds__(256, RB == 1 ? 4 : 2) void rows_q8_kernel(const Att
         }
       uint32_t at = va;
       asm volatile("" : "+v"(at));
+      float one = 1.0f;
+      if constexpr (CODE == INT8) asm volatile("" : "+v"(one));  // or bytes go through integers
 #pragma unroll
       for (int d = 0; d < DIM / 16; ++d) {
         if (d % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // few registers at a time
         const u32x2v_t w = lds_read_tr8(at ^ 16 * d);
-        const u32x2v_t lo = Code<CODE>::widen16(bf16{}, w[0], 1.0f), hi = Code<CODE>::widen16(bf16{}, w[1], 1.0f);
+        const u32x2v_t lo = Code<CODE>::widen16(bf16{}, w[0], one), hi = Code<CODE>::widen16(bf16{}, w[1], one);
         const bf16x8_t v = __builtin_bit_cast(bf16x8_t, u32x4v_t{lo[0], lo[1], hi[0], hi[1]});
 #pragma unroll
         for (int b = 0; b < RB; ++b) {

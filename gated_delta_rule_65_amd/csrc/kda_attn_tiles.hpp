@@ -49,7 +49,7 @@ template <int P> __device__ __forceinline__ int vswz(int r) {
 // CODE: the codes of a cache in 8 bits (A is AttnQ8Launch), or NO_CODE.
 constexpr int NO_CODE = -1;
 template <typename A, typename E, int DIM, int NW, int CODE>
-__global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const A a) {
+__global__ __launch_bounds__(64 * NW, CODE != NO_CODE && DIM == 64 ? 3 : 2) void tiles_kernel(const A a) {
   typedef typename Half<E>::frag frag;
   constexpr int P = DIM / 8;            // 16-byte pieces per row
   constexpr int NI = P / NW;            // DMA instructions per wave and tile, K or V
@@ -189,61 +189,90 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const A a) {
     return valid;
   };
 
-  // A cache in 8 bits: each thread fetches NX pieces of 16 codes of a tile, K's before V's,
-  // and their scales, into registers while the tile before is worked on, and then widens them into
-  // the tile that the matrix instructions read.
-  constexpr int PC = DIM / 16, NX = Q8 ? 2 * PC / NW : 1;
-  u32x4v_t codes[PAIR][NX];
-  float scale[PAIR][NX];
-  auto fetch = [&](int base, uint64_t valid, int j, int x0, int x1) __attribute__((always_inline)) {
+  // A cache in 8 bits: each thread fetches NX pieces of 16 codes of a tile and their scales into
+  // registers, half of them K's and then the same rows of V (or, where there is one, waves
+  // of the first half K's and the others V's), and a step later widens them into a tile
+  // that the matrix instructions read.
+  constexpr int PC = DIM / 16, NX = Q8 ? 2 * PC / NW : 1, NR = NX > 1 ? NX / 2 : 1;
+  u32x4v_t codes[NX];
+  float scale[NX];
+  const int wrow = (NX > 1 ? wave : wave % (NW / 2)) * (64 / PC);  // the wave's first row; others 64 NW / PC on
+  auto of_v = [&](int x) __attribute__((always_inline)) { return NX > 1 ? x >= NR : wave >= NW / 2; };
+  // Addresses are integers: a generic pointer would make every LDS read wait for the loads.
+  auto get = [&](int x, uint64_t cp, uint64_t sp) __attribute__((always_inline)) {
+    codes[x] = *(const __attribute__((address_space(1))) u32x4v_t*)cp;
+    scale[x] = *(const __attribute__((address_space(1))) float*)sp;
+  };
+  const int64_t scale_page = [&] {
+    if constexpr (Q8) return (int64_t)a.hkv * a.scales.per_page * 4;
+    else return (int64_t)0;
+  }();
+  auto pool_of = [&](bool v) __attribute__((always_inline)) { return (uint64_t)(v ? vbase : kbase); };
+  auto scales_of = [&](bool v) __attribute__((always_inline)) -> uint64_t {
+    if constexpr (Q8) return (uint64_t)((v ? a.scales.v : a.scales.k) + (int64_t)kvh * a.scales.per_page);
+    else return 0;
+  };
+  // Piece x where a load's rows share a page and every key is there: scalar work but for the scales.
+  // V's use what the same rows of K have worked out.  For another tile it loads something that the
+  // page or page 0 holds (16 bytes of a row, where rows of a load may lie on two), with no branch.
+  const bool pages_fit = a.page.d % (64 / PC) == 0;
+  const uint32_t fetch_byte = pages_fit ? 16 * lane : 0, fetch_row = pages_fit ? lane / PC : 0;
+  uint32_t fpage[NR], fscale[NR];
+  int foff[NR];
+  auto fetch_whole = [&](int base, int x) __attribute__((always_inline)) {
     if constexpr (Q8) {
-      const int lane = again(threadIdx.x & 63);  // or addresses would be kept for every x
-      const int64_t scale_page = (int64_t)a.hkv * a.scales.per_page;
-      const bool whole = a.page.d % (64 / PC) == 0 && valid == ~0ull;  // one page per load
-#pragma unroll
-      for (int x = x0; x < x1; ++x) {
-        const int first = 64 * (wave + NW * x), r0 = first % (KT * PC) / PC;
-        const bool is_v = first >= KT * PC;
-        const char* const pool = is_v ? vbase : kbase;
-        const int64_t stride = is_v ? a.v_page : a.k_page;
-        const float* const sc = (is_v ? a.scales.v : a.scales.k) + (int64_t)kvh * a.scales.per_page;
-        if (whole) {
-          const int key = base + r0, pg = (int)fdiv(key, a.page), off = key - pg * (int)a.page.d;
-          const int64_t page = pages.uniform_at(pg);
-          codes[j][x] = *(const u32x4v_t*)(pool + page * stride + (int64_t)off * DIM + 16 * lane);
-          scale[j][x] = sc[page * scale_page + fdiv(off + lane / PC, a.scales.block)];
-        } else {
-          const int row = r0 + lane / PC, key = base + row, pg = (int)fdiv(key, a.page);
-          const int off = key - pg * (int)a.page.d;
-          const int64_t page = pages.at(pg);
-          const char* cp = pool + page * stride + (int64_t)off * DIM + 16 * (lane % PC);
-          const float* sp = sc + page * scale_page + fdiv(off, a.scales.block);
-          if (!((valid >> row) & 1)) {
-            cp = (const char*)&attn_zero;
-            sp = (const float*)&attn_zero;
-          }
-          codes[j][x] = *(const u32x4v_t*)cp;
-          scale[j][x] = *sp;
-        }
+      const int r = x % NR;
+      const bool v = of_v(x);
+      if (x < NR) {
+        const int key = base + wrow + r * (64 * NW / PC), pg = (int)fdiv(key, a.page);
+        foff[r] = key - pg * (int)a.page.d;
+        fpage[r] = (uint32_t)max(pages.uniform_at(pg), 0);
+        fscale[r] = 4 * fdiv(foff[r] + fetch_row, a.scales.block);
       }
+      // (a uniform address and an offset of 32 bits: no registers for sums of the two)
+      typedef const __attribute__((address_space(1))) char* bytes_t;
+      const bytes_t cp = (bytes_t)(pool_of(v) + fpage[r] * (uint64_t)(v ? a.v_page : a.k_page) +
+                                   (uint64_t)foff[r] * DIM);
+      const bytes_t sp = (bytes_t)(scales_of(v) + fpage[r] * (uint64_t)scale_page);
+      codes[x] = *(const __attribute__((address_space(1))) u32x4v_t*)(cp + fetch_byte);
+      scale[x] = *(const __attribute__((address_space(1))) float*)(sp + fscale[r]);
     }
   };
-  auto widen = [&](int stage, int j, int x0, int x1) __attribute__((always_inline)) {
+  auto fetch = [&](int base, uint64_t valid, int x) __attribute__((always_inline)) {  // any tile
     if constexpr (Q8) {
-      const int lane = again(threadIdx.x & 63);
+      const int ln = again(lane);  // or addresses would be kept for every x
+      const int row = wrow + x % NR * (64 * NW / PC) + ln / PC, key = base + row;
+      const int pg = (int)fdiv(key, a.page), off = key - pg * (int)a.page.d;
+      const int64_t page = pages.at(pg);
+      const bool v = of_v(x), is = (valid >> row) & 1;
+      get(x, is ? pool_of(v) + page * (v ? a.v_page : a.k_page) + (int64_t)off * DIM + 16 * (ln % PC)
+                : (uint64_t)&attn_zero,
+          is ? scales_of(v) + page * scale_page + 4 * fdiv(off, a.scales.block) : (uint64_t)&attn_zero);
+    }
+  };
+  // Where the first half of this lane's piece goes in stage 0; the second is the neighbour.  Sixteen
+  // lanes write rows whose V swizzles are all even: half of the rows write their second
+  // half first, so that the sixteen pieces fall into different banks.
+  const int crow = wrow + lane / PC, vflip = P == 16 ? crow & 1 : (crow >> 1) & 1;
+  const uint32_t kput = lds_addr(&smem_k[0][crow * P + (2 * (lane % PC) ^ kswz<P>(crow))]);
+  const uint32_t vput = lds_addr(&smem_v[0][crow * P + ((2 * (lane % PC) + vflip) ^ vswz<P>(crow))]);
+  static_assert(!Q8 || NR == 1 || 64 * NW / PC % 16 == 0, "a thread's rows agree modulo 16");
+  auto widen = [&](int at, int x, int y) __attribute__((always_inline)) {  // half y; at: bytes of the stage
+    if constexpr (Q8) {
+      const bool v = of_v(x);
+      const bool other = v && vflip;  // the halves in turn
+      const uint32_t w0 = other ? codes[x][2 - 2 * y] : codes[x][2 * y];
+      const uint32_t w1 = other ? codes[x][3 - 2 * y] : codes[x][2 * y + 1];
+      const u32x2v_t lo = Code<CODE>::widen16(E{}, w0, scale[x]), hi = Code<CODE>::widen16(E{}, w1, scale[x]);
+      const uint32_t to = ((v ? vput : kput) ^ 16 * y) + at + x % NR * (64 * NW / PC) * ROW;
+      *(__attribute__((address_space(3))) u32x4v_t*)(uintptr_t)to = u32x4v_t{lo[0], lo[1], hi[0], hi[1]};
+    }
+  };
+  auto widen_all = [&](int at) __attribute__((always_inline)) {
 #pragma unroll
-      for (int x = x0; x < x1; ++x) {
-        const int first = 64 * (wave + NW * x), row = (first % (KT * PC) + lane) / PC;
-        const bool is_v = first >= KT * PC;
-        uint4* const dst = (is_v ? smem_v[stage] : smem_k[stage]) + row * P;
-        const int swz = is_v ? vswz<P>(row) : kswz<P>(row);
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const u32x2v_t lo = Code<CODE>::widen16(E{}, codes[j][x][2 * y], scale[j][x]);
-          const u32x2v_t hi = Code<CODE>::widen16(E{}, codes[j][x][2 * y + 1], scale[j][x]);
-          dst[(2 * (lane % PC) + y) ^ swz] = make_uint4(lo[0], lo[1], hi[0], hi[1]);
-        }
-      }
+    for (int x = 0; x < NX; ++x) {
+      widen(at, x, 0);
+      widen(at, x, 1);
     }
   };
 
@@ -272,8 +301,25 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const A a) {
   // The products of a slot.  The scheduler is told to keep AHEAD fragments' reads in
   // flight: left to itself it waits for each one right before its product.
   constexpr int AHEAD = 3, NS = 2 * QS, NV = 4 * DV;
-  auto scores = [&](int stage) __attribute__((always_inline)) {
+  // Over codes the order is spelled out (beside codes on their way the scheduler gives it up), with
+  // other work between the products: `fill` of a step.
+  auto nothing = [](int) {};
+  auto scores = [&](int stage, auto fill) __attribute__((always_inline)) {
     clear_scores();
+    if constexpr (Q8) {
+      u32x4v_t f[AHEAD];
+#pragma unroll
+      for (int n = 0; n < NS + AHEAD; ++n) {
+        if (n >= AHEAD) {
+          const int x = (n - AHEAD) / 2, k = (n - AHEAD) % 2;
+          s[k] = Half<E>::mma32(__builtin_bit_cast(frag, f[n % AHEAD]), q[x], s[k]);
+        }
+        if (n < NS) f[n % AHEAD] = lds_read16(ka[n / 2] + stage * STAGE + 32 * (n % 2) * ROW);
+        fill(n);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      return;
+    }
 #pragma unroll
     for (int n = 0; n < NS; ++n) score(stage, n);
     __builtin_amdgcn_sched_group_barrier(DS_READ, AHEAD, 0);
@@ -284,7 +330,27 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const A a) {
     }
     __builtin_amdgcn_sched_group_barrier(MFMA, AHEAD, 0);
   };
-  auto values = [&](int stage) __attribute__((always_inline)) {
+  auto values = [&](int stage, auto fill) __attribute__((always_inline)) {
+    if constexpr (Q8) {
+      s16x4_t u[AHEAD], w[AHEAD];
+#pragma unroll
+      for (int n = 0; n < NV + AHEAD; ++n) {
+        if (n >= AHEAD) {
+          const int m = n % AHEAD, kc = (n - AHEAD) / DV, d = (n - AHEAD) % DV;
+          typedef short s16x8_t __attribute__((ext_vector_type(8)));
+          const s16x8_t z = {u[m][0], u[m][1], u[m][2], u[m][3], w[m][0], w[m][1], w[m][2], w[m][3]};
+          o[d] = Half<E>::mma32(__builtin_bit_cast(frag, z), p[kc], o[d]);
+        }
+        if (n < NV) {
+          const uint32_t at = va[n % DV] + stage * STAGE + 16 * (n / DV) * ROW;
+          u[n % AHEAD] = lds_read_tr(at);
+          w[n % AHEAD] = lds_read_tr(at + 8 * ROW);
+        }
+        fill(n);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      return;
+    }
 #pragma unroll
     for (int n = 0; n < NV; ++n) value(stage, n);
     __builtin_amdgcn_sched_group_barrier(DS_READ, 2 * AHEAD, 0);
@@ -392,6 +458,30 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const A a) {
 #pragma unroll
     for (int d = 0; d < DV; ++d) va[d] += by;
   };
+  // The queries come through the half of the ring that the first tiles leave free,
+  // 32 rows to a wave, laid out as K rows are: whole rows at a time, where fragments
+  // straight from memory touch each row in eight pieces (24 ragged prompts of 33515
+  // tokens: 822 us against 849 us).
+  auto ask_queries = [&]() __attribute__((always_inline)) {
+    uint4* const mine = wave < NW / 2 ? &smem_k[PAIR][wave * 32 * P] : &smem_v[PAIR][(wave - NW / 2) * 32 * P];
+#pragma unroll
+    for (int x = 0; x < P / 2; ++x) {
+      const int row = (64 * x + lane) / P;
+      const int lo = __builtin_amdgcn_ds_bpermute(4 * row, (int)qrow);
+      const int hi = __builtin_amdgcn_ds_bpermute(4 * row, (int)(qrow >> 32));
+      const int64_t at = ((int64_t)hi << 32) | (uint32_t)lo;
+      const char* g = (const char*)a.q + 2 * at + 16 * (lane % P ^ kswz<P>(row));
+      if (hi < 0) g = (const char*)&attn_zero;
+      dma16(g, lds_addr(mine + 64 * x));
+    }
+    return mine;
+  };
+  auto take_queries = [&](const uint4* mine) __attribute__((always_inline)) {
+    dma_wait<0>();
+#pragma unroll
+    for (int x = 0; x < QS; ++x)
+      q[x] = __builtin_bit_cast(frag, lds_read16(ka[x] + lds_addr(mine) - lds_addr(&smem_k[0][0])));
+  };
   // PAIR tiles between barriers, while the DMA fills the other half of the ring.  A
   // wave without rows (in a request's last tile) does its part of the loads only.
   auto walk = [&](auto busy) __attribute__((always_inline)) {
@@ -404,42 +494,12 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const A a) {
       for (int j = 0; j < PAIR; ++j) {
         next[j] = 0;
         nbase[j] = range.base(i + j);
-        if (i + j < t1) {
-          if constexpr (Q8) {
-            next[j] = locate(nbase[j]);
-            fetch(nbase[j], next[j], j, 0, NX);
-          } else {
-            next[j] = issue(nbase[j], half * PAIR + j);
-          }
-        }
+        if (i + j < t1) next[j] = issue(nbase[j], half * PAIR + j);
       }
     };
-    auto arrive = [&](int i, int half) __attribute__((always_inline)) {  // what load(i, half) asked for
-#pragma unroll
-      for (int j = 0; j < PAIR; ++j)
-        if (i + j < t1) widen(half * PAIR + j, j, 0, NX);
-    };
-    // The queries come through the half of the ring that the first tiles leave free,
-    // 32 rows to a wave, laid out as K rows are: whole rows at a time, where fragments
-    // straight from memory touch each row in eight pieces (24 ragged prompts of 33515
-    // tokens: 822 us against 849 us).
-    uint4* const mine = wave < NW / 2 ? &smem_k[PAIR][wave * 32 * P] : &smem_v[PAIR][(wave - NW / 2) * 32 * P];
-#pragma unroll
-    for (int x = 0; x < P / 2; ++x) {
-      const int row = (64 * x + lane) / P;
-      const int lo = __builtin_amdgcn_ds_bpermute(4 * row, (int)qrow);
-      const int hi = __builtin_amdgcn_ds_bpermute(4 * row, (int)(qrow >> 32));
-      const int64_t at = ((int64_t)hi << 32) | (uint32_t)lo;
-      const char* g = (const char*)a.q + 2 * at + 16 * (lane % P ^ kswz<P>(row));
-      if (hi < 0) g = (const char*)&attn_zero;
-      dma16(g, lds_addr(mine + 64 * x));
-    }
+    uint4* const mine = ask_queries();
     load(t0, 0);
-    if constexpr (Q8) arrive(t0, 0);
-    dma_wait<0>();
-#pragma unroll
-    for (int x = 0; x < QS; ++x)
-      q[x] = __builtin_bit_cast(frag, lds_read16(ka[x] + lds_addr(mine) - lds_addr(&smem_k[0][0])));
+    take_queries(mine);
     int half = 0;
 #pragma unroll 1
     for (int i = t0; i < t1; i += PAIR, half ^= 1) {
@@ -451,24 +511,103 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const A a) {
       // these tiles have landed for every wave, and every wave is done with the last
       tile_barrier<0>();
       load(i + PAIR, half ^ 1);
-      if constexpr (!BUSY) {
-        if constexpr (Q8) arrive(i + PAIR, half ^ 1);
-        continue;
-      }
+      if constexpr (!BUSY) continue;
 #pragma unroll
       for (int j = 0; j < PAIR; ++j) {
         if (i + j >= t1) break;
         __builtin_amdgcn_s_setprio(1);
-        scores(j);
+        scores(j, nothing);
         __builtin_amdgcn_s_setprio(0);
         if (!whole(base[j], valid[j])) hide(base[j], valid[j]);
         softmax();
         __builtin_amdgcn_s_setprio(1);
-        values(j);
+        values(j, nothing);
         __builtin_amdgcn_s_setprio(0);
       }
-      if constexpr (Q8) arrive(i + PAIR, half ^ 1);
       turn(half ? -PAIR * STAGE : PAIR * STAGE);
+    }
+    if (BUSY && half) turn(-PAIR * STAGE);
+  };
+  // The same over codes.  Tile t's step widens the codes of tile t + PAIR (fetched during the step
+  // before) among its scores, into the half of the ring that the barrier has set free, and
+  // fetches those of the tile after that among its values.
+  auto walk_codes = [&](auto busy) __attribute__((always_inline)) {
+    constexpr bool BUSY = decltype(busy)::value;
+    constexpr int LOOK = PAIR + 1;
+    clear();
+    uint64_t valid[LOOK + 1];  // the keys of tiles t .. t + LOOK
+    int base[LOOK + 1];        // and where they start
+    auto find = [&](int t, int k) __attribute__((always_inline)) {
+      base[k] = range.base(t);
+      valid[k] = locate(base[k]);
+    };
+    auto fetch_any = [&](int k) __attribute__((always_inline)) {
+#pragma unroll
+      for (int x = 0; x < NX; ++x) fetch(base[k], valid[k], x);
+    };
+    const uint4* const mine = ask_queries();
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+      codes[x] = u32x4v_t{0, 0, 0, 0};
+      scale[x] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < LOOK; ++j) {
+      base[j] = 0;
+      valid[j] = 0;
+      if (t0 + j < t1) {
+        find(t0 + j, j);
+        fetch_any(j);
+        if (j < PAIR) widen_all(j * STAGE);
+      }
+    }
+    take_queries(mine);
+    int half = 0;
+#pragma unroll 1
+    for (int i = t0; i < t1; i += PAIR, half ^= 1) {
+      // these tiles are there for every wave, and every wave is done with the last
+      lds_wait();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" : : : "memory");
+      const int there = (half ^ 1) * (PAIR * STAGE);
+#pragma unroll
+      for (int j = 0; j < PAIR; ++j) {
+        const int t = i + j;
+        if (t >= t1) break;
+        if constexpr (BUSY) {
+          __builtin_amdgcn_s_setprio(1);
+          scores(j, [&](int n) __attribute__((always_inline)) {
+            const int m = n - AHEAD;
+            if (m >= 0 && m < 2 * NX) widen(there + j * STAGE, m / 2, m % 2);
+          });
+          __builtin_amdgcn_s_setprio(0);
+          if (!whole(base[0], valid[0])) hide(base[0], valid[0]);
+          softmax();
+        } else {
+          widen_all(there + j * STAGE);
+        }
+        valid[LOOK] = 0;
+        base[LOOK] = 0;
+        const bool more = t + LOOK < t1;
+        if (more) find(t + LOOK, LOOK);
+        if constexpr (BUSY) {
+          __builtin_amdgcn_s_setprio(1);
+          values(j, [&](int n) __attribute__((always_inline)) {
+            if (n % 2 == 0 && n / 2 < NX) fetch_whole(base[LOOK], n / 2);
+          });
+          __builtin_amdgcn_s_setprio(0);
+        } else {
+#pragma unroll
+          for (int x = 0; x < NX; ++x) fetch_whole(base[LOOK], x);
+        }
+        if (more && !(pages_fit && valid[LOOK] == ~0ull)) fetch_any(LOOK);
+#pragma unroll
+        for (int k = 0; k < LOOK; ++k) {
+          valid[k] = valid[k + 1];
+          base[k] = base[k + 1];
+        }
+      }
+      if constexpr (BUSY) turn(half ? -PAIR * STAGE : PAIR * STAGE);
     }
     if (BUSY && half) turn(-PAIR * STAGE);
   };
@@ -492,8 +631,9 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const A a) {
         valid = locate(base);
 #pragma unroll
         for (int x = 0; x < NX; ++x) {
-          fetch(base, valid, 0, x, x + 1);
-          widen(0, 0, x, x + 1);
+          fetch(base, valid, x);
+          widen(0, x, 0);
+          widen(0, x, 1);
           __builtin_amdgcn_sched_barrier(0);  // few registers at a time
         }
       } else {
@@ -501,15 +641,20 @@ __global__ __launch_bounds__(64 * NW, 2) void tiles_kernel(const A a) {
       }
       dma_wait<0>();
       __syncthreads();
-      scores(0);
+      scores(0, nothing);
       hide(base, valid);
       softmax();
-      if (whole(base, valid)) values(0);
+      if (whole(base, valid)) values(0, nothing);
       else values_by_key(base, 0, valid);
     }
   };
-  if (32 * wave < rows) walk(std::true_type{});
-  else walk(std::false_type{});
+  if constexpr (Q8) {
+    if (32 * wave < rows) walk_codes(std::true_type{});
+    else walk_codes(std::false_type{});
+  } else {
+    if (32 * wave < rows) walk(std::true_type{});
+    else walk(std::false_type{});
+  }
   // a hidden infinity or NaN of V has spoilt the sums of its tile: once more, carefully
   float z = 0.0f;  // becomes NaN if any sum is not finite
 #pragma unroll

@@ -134,7 +134,7 @@ def _call(fn, args, dev):
         with torch.cuda.device(dev):
             st = fn(ctypes.byref(args))
     if st != KDA_OK:
-        _raise(_lib, st)
+        _raise(binding.load_library(), st)
 
 
 def _int32(x, n, name, dev):
