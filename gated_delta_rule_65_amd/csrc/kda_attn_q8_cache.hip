@@ -59,12 +59,12 @@ __device__ __forceinline__ float max_wave(float x) {
   return x;
 }
 
-// WAVES: waves that share a block, 1 or 4.
+// WAVES: waves that share a block.
 template <typename E, int DIM, int CODE, int WAVES>
-__global__ __launch_bounds__(256) void append_q8_kernel(const CacheQ8Launch a, uint32_t units) {
+__global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void append_q8_kernel(const CacheQ8Launch a, uint32_t units) {
   constexpr int LPR = DIM / 8, RPL = 64 / LPR * WAVES;  // lanes per row, rows per step
   constexpr int HOLD = 4;                               // steps held in registers
-  __shared__ float s_top[2][4];
+  __shared__ float s_top[2][WAVES];
   const int lane = threadIdx.x & 63, wave = wave_of();
   const uint32_t w = WAVES == 1 ? blockIdx.x * 4 + wave : blockIdx.x;
   if (w >= units) return;
@@ -129,8 +129,11 @@ __global__ __launch_bounds__(256) void append_q8_kernel(const CacheQ8Launch a, u
       s_top[1][wave] = vtop;
     }
     __syncthreads();
-    ktop = fmaxf(fmaxf(s_top[0][0], s_top[0][1]), fmaxf(s_top[0][2], s_top[0][3]));
-    vtop = fmaxf(fmaxf(s_top[1][0], s_top[1][1]), fmaxf(s_top[1][2], s_top[1][3]));
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+      ktop = fmaxf(ktop, s_top[0][i]);
+      vtop = fmaxf(vtop, s_top[1][i]);
+    }
   }
   const float ks = fmaxf(Code<CODE>::least_scale(ktop), ks0);
   const float vs = fmaxf(Code<CODE>::least_scale(vtop), vs0);
@@ -169,29 +172,54 @@ __global__ __launch_bounds__(256) void append_q8_kernel(const CacheQ8Launch a, u
   }
 }
 
-constexpr int READ_ROWS = 16;
-
-template <typename E, int CODE> __device__ __forceinline__ void store_scaled(E* p, uint2 u, float s) {
-  float x[4], y[4];
-  Code<CODE>::widen(u.x, x);
-  Code<CODE>::widen(u.y, y);
-  if constexpr (sizeof(E) == 4) {
-    store4(p, x[0] * s, x[1] * s, x[2] * s, x[3] * s);
-    store4(p + 4, y[0] * s, y[1] * s, y[2] * s, y[3] * s);
-  } else {
-    typename Half<E>::frag f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      Half<E>::set(f, i, x[i] * s);
-      Half<E>::set(f, 4 + i, y[i] * s);
+// A thread's 16 bytes of a row: the values of 4 or 8 codes.
+template <typename E, int CODE> struct Out {
+  static constexpr int N = 16 / (int)sizeof(E);
+  uint32_t u[N / 4];
+  float s;
+  __device__ __forceinline__ void load(const uint8_t* p, const float* scale) {
+    if constexpr (N == 4) {
+      u[0] = *(const uint32_t*)p;
+    } else {
+      const uint2 w = *(const uint2*)p;
+      u[0] = w.x, u[1] = w.y;
     }
-    *reinterpret_cast<typename Half<E>::frag*>(p) = f;
+    s = *scale;
   }
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) u[i] = 0;
+    s = 0.0f;
+  }
+  __device__ __forceinline__ void store(E* p) const {
+    float x[N];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      float y[4];
+      Code<CODE>::widen(u[i], y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[4 * i + j] = y[j] * s;
+    }
+    if constexpr (N == 4) {
+      store4(p, x[0], x[1], x[2], x[3]);
+    } else {
+      typename Half<E>::frag f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) Half<E>::set(f, i, x[i]);
+      *reinterpret_cast<typename Half<E>::frag*>(p) = f;
+    }
+  }
+};
+
+// Rows of a unit: few, so that even a small call has a few loads per thread and many units
+// (33000 rows as fp32: 66 us with 4 rows, 76 with 16, 81 with 32; stores that bypass the
+// caches 132).
+constexpr int READ_ROWS = 4;
 
 template <typename E, int DIM, int CODE>
 __global__ __launch_bounds__(256) void read_q8_kernel(const CacheQ8Launch a, FastDiv per_token) {
-  constexpr int LPR = DIM / 8;
+  typedef Out<E, CODE> Piece;
+  constexpr int LPR = DIM / Piece::N;
   __shared__ int64_t s_k[READ_ROWS], s_v[READ_ROWS], s_s[READ_ROWS];  // bytes, bytes, scales; -1: no page
   const int tid = threadIdx.x, lane = tid & 63;
   const int item = (int)blockIdx.x;
@@ -221,32 +249,29 @@ __global__ __launch_bounds__(256) void read_q8_kernel(const CacheQ8Launch a, Fas
   // AT_ONCE steps' loads go out together: a few rows are bound by latency
   constexpr int AT_ONCE = 4;
   for (uint32_t x0 = tid; x0 < total; x0 += 256 * AT_ONCE) {
-    uint2 ku[AT_ONCE], vu[AT_ONCE];
-    float ks[AT_ONCE], vs[AT_ONCE];
+    Piece k[AT_ONCE], v[AT_ONCE];
     int64_t to[AT_ONCE];
 #pragma unroll
     for (int j = 0; j < AT_ONCE; ++j) {
       const uint32_t x = x0 + 256 * j;
-      ku[j] = vu[j] = make_uint2(0, 0);
-      ks[j] = vs[j] = 0.0f;
+      k[j].zero();
+      v[j].zero();
       if (x < total) {
         const uint32_t t = fdiv(x, per_token), p = x - t * per_token.d;
-        const int h = (int)(p / LPR), col = 8 * (int)(p % LPR);
-        to[j] = (int64_t)(start + first + (int)t) * a.hkv * DIM + 8 * (int64_t)p;
-        const int64_t kb = s_k[t];
+        const int h = (int)(p / LPR), col = Piece::N * (int)(p % LPR);
+        to[j] = (int64_t)(start + first + (int)t) * a.hkv * DIM + Piece::N * (int64_t)p;
+        const int64_t kb = s_k[t], at = s_s[t] + (int64_t)h * a.per_page;
         if (kb >= 0) {
-          ku[j] = *(const uint2*)((const uint8_t*)a.kc + kb + h * head + col);
-          vu[j] = *(const uint2*)((const uint8_t*)a.vc + s_v[t] + h * head + col);
-          ks[j] = a.ks[s_s[t] + (int64_t)h * a.per_page];
-          vs[j] = a.vs[s_s[t] + (int64_t)h * a.per_page];
+          k[j].load((const uint8_t*)a.kc + kb + h * head + col, a.ks + at);
+          v[j].load((const uint8_t*)a.vc + s_v[t] + h * head + col, a.vs + at);
         }
       }
     }
 #pragma unroll
     for (int j = 0; j < AT_ONCE; ++j) {
       if (x0 + 256 * j >= total) break;
-      store_scaled<E, CODE>((E*)a.ko + to[j], ku[j], ks[j]);
-      store_scaled<E, CODE>((E*)a.vo + to[j], vu[j], vs[j]);
+      k[j].store((E*)a.ko + to[j]);
+      v[j].store((E*)a.vo + to[j]);
     }
   }
 }
@@ -254,18 +279,19 @@ __global__ __launch_bounds__(256) void read_q8_kernel(const CacheQ8Launch a, Fas
 template <typename E, int DIM, int CODE> hipError_t append_go(const CacheQ8Launch& L) {
   const uint32_t items = (uint32_t)L.total / L.block.d + 2u * (uint32_t)L.n;
   const uint32_t units = items * (uint32_t)L.hkv;
+  const hipStream_t stream = (hipStream_t)L.stream;
   if (L.block.d <= 16)
-    hipLaunchKernelGGL((append_q8_kernel<E, DIM, CODE, 1>), dim3((units + 3) / 4), dim3(256), 0,
-                       (hipStream_t)L.stream, L, units);
+    hipLaunchKernelGGL((append_q8_kernel<E, DIM, CODE, 1>), dim3((units + 3) / 4), dim3(256), 0, stream, L, units);
+  else if (L.block.d <= 32)
+    hipLaunchKernelGGL((append_q8_kernel<E, DIM, CODE, 2>), dim3(units), dim3(128), 0, stream, L, units);
   else
-    hipLaunchKernelGGL((append_q8_kernel<E, DIM, CODE, 4>), dim3(units), dim3(256), 0,
-                       (hipStream_t)L.stream, L, units);
+    hipLaunchKernelGGL((append_q8_kernel<E, DIM, CODE, 4>), dim3(units), dim3(256), 0, stream, L, units);
   return hipGetLastError();
 }
 template <typename E, int DIM, int CODE> hipError_t read_go(const CacheQ8Launch& L) {
-  const uint32_t items = (uint32_t)L.total / READ_ROWS + (uint32_t)L.n;
+  const uint32_t items = (uint32_t)(L.total / READ_ROWS) + (uint32_t)L.n;
   hipLaunchKernelGGL((read_q8_kernel<E, DIM, CODE>), dim3(items), dim3(256), 0, (hipStream_t)L.stream, L,
-                     fast_div((uint32_t)(L.hkv * DIM / 8)));
+                     fast_div((uint32_t)(L.hkv * DIM / Out<E, CODE>::N)));
   return hipGetLastError();
 }
 
