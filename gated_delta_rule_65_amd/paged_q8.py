@@ -114,12 +114,11 @@ def _codes(k_cache, v_cache, k_scale, v_scale):
             page_size, dim, page_size // blocks)
 
 
-def _one_device(dev, **tensors):
-    """As _same_device, for tensors that are all there: their indexes first, which cost less."""
-    on = -1 if dev.type == "cpu" else dev.index
-    for t in tensors.values():
-        if t.get_device() != on:
-            _same_device(dev, **tensors)
+def _cache_device(on, k_cache, v_cache, k_scale, v_scale, block_table):
+    """Whether a cache and its table are on the device of this index (-1 the host's); indexes cost
+    less than devices."""
+    return (k_cache.get_device() == on and v_cache.get_device() == on and k_scale.get_device() == on
+            and v_scale.get_device() == on and block_table.get_device() == on)
 
 
 def _requests(block_table, cu_seqlens, seq_lens, dev):
@@ -160,8 +159,10 @@ def kv_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqle
     dev = k.device
     n, cu, seq, stride, cols = _requests(block_table, cu_seqlens, seq_lens, dev)
     ks, vs = _rows_stride("k", k), _rows_stride("v", v)
-    _one_device(dev, v=v, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-                block_table=block_table)
+    on = k.get_device()
+    if v.get_device() != on or not _cache_device(on, k_cache, v_cache, k_scale, v_scale, block_table):
+        _same_device(dev, v=v, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                     block_table=block_table)
     _on_gpu(dev)
     lib = _lib or load_library()
     _call(lib.kda_kv_append_q8, KvAppendQ8Args(
@@ -204,8 +205,9 @@ def kv_read_q8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_
             _need(t.shape == shape, f"{name} must have shape {list(shape)}")
             _need(t.dtype is dtype, f"{name} must have k_out's dtype", TypeError)
             _need(t.is_contiguous(), f"{name} must be contiguous")
-        _one_device(dev, k_out=k_out, v_out=v_out)
-    _one_device(dev, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table)
+        _same_device(dev, k_out=k_out, v_out=v_out)
+    if not _cache_device(k_cache.get_device(), k_cache, v_cache, k_scale, v_scale, block_table):
+        _same_device(dev, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table)
     _on_gpu(dev)
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=dev)
@@ -298,8 +300,9 @@ def paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_se
         _need(lse.is_contiguous(), "lse must be contiguous")
     if workspace is not None:
         _need(workspace.is_contiguous(), "workspace must be contiguous")
-    _one_device(dev, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
-                block_table=block_table)
+    if not _cache_device(q.get_device(), k_cache, v_cache, k_scale, v_scale, block_table):
+        _same_device(dev, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                     block_table=block_table)
     if not (output is None and lse is None and workspace is None):
         _same_device(dev, output=output, lse=lse, workspace=workspace)
     _on_gpu(dev)
