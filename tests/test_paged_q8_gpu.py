@@ -176,9 +176,10 @@ def test_append_and_read_of_strided_rows_and_pools(code, dt):
                 assert np.array_equal(out[x].cpu().double().numpy(), cache.row(side, int(wide[i, 2 + pos // page]), pos % page))
 
 
-def test_many_requests_and_offsets_that_decrease():
+@pytest.mark.parametrize("n", [63, 64, 65, 200, 256, 257, 3000])
+def test_many_requests_and_offsets_that_decrease(n):
     """More requests than a wave looks through at once; offsets out of order write nothing wrong."""
-    n, page, hkv, dim = 3000, 4, 1, 64
+    page, hkv, dim = 4, 1, 64
     g = torch.Generator().manual_seed(2)
     seq = torch.randint(0, 8, (n,), generator=g)
     new = torch.minimum(torch.randint(0, 3, (n,), generator=g), seq)
@@ -382,6 +383,26 @@ def test_lengths_below_the_new_tokens_and_past_the_table(code, new):
     c.seq[0] = new - 1                        # the first row lies below position 0
     c.keys[0], c.values[0] = c.keys[0][:new - 1], c.values[0][:new - 1]
     check(c, 16, attend(c, cache))
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("code", CODES)
+def test_more_new_tokens_than_the_hint_says(code, dt):
+    """A hint of one new token for chunks: the rows of a request in turns of 16, hidden NaN codes kept out."""
+    c, cache = Q.make([100, 0, 7], [70, 33, 1], 4, 2, 128, 16, 8, dt, code, seed=14)
+    check(c, 16, attend(c, cache, max_new_len=1))
+    check(c, 16, attend(c, cache, 40, 3, max_new_len=1, splits=3), 40, 3)
+    if code == "e4m3":
+        for i, pos, side in ((0, 169, 1), (0, 120, 1), (1, 32, 0)):
+            cache.codes[side][int(c.table[i, pos // 16]), 1, pos % 16, 77] = 0xff
+            (c.keys, c.values)[side][i][pos, 1, 77] = float("nan")
+        out, _ = attend(c, cache, max_new_len=1)
+        with np.errstate(all="ignore"):
+            ref, _, tol, _ = R.attention(c, 16, 128 ** -0.5)
+        o = out.double().numpy()
+        fine = np.isfinite(ref)
+        assert np.array_equal(np.isfinite(o), fine)
+        assert np.all(np.abs(o[fine] - ref[fine]) <= tol[fine])
 
 
 def test_scales_far_apart_and_tiny():
