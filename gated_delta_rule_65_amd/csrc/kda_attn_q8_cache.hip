@@ -2,19 +2,25 @@
 //
 // Append.  A block's scale follows the largest magnitude among its new rows, and its
 // earlier rows where it already has some, so the unit of work is (block, head): a wave, or
-// a workgroup where blocks are long, holds the block's new rows in registers, takes their
-// largest magnitude, settles the scale and writes the codes.  No block belongs to two units, so
+// two or four of them where blocks are long, hold the block's new rows in registers, take their
+// largest magnitude, settle the scale and write the codes.  No block belongs to two units, so
 // there are no atomics, and the rows are read once.  Request i's units start at
-// floor(cu[i] / block) + 2 i, which leaves it as many as its rows can touch.
+// floor(cu[i] / block) + 2 i, which leaves it as many as its rows can touch.  Bound by HBM
+// where rows are many: 30669 tokens of 8 heads of 128 bf16 channels (126 MB in, 63 MB out) 46 us,
+// 4.1 TB/s, in blocks of 16, 32 (one wave a block: 51 us, four: 59) or 64; by
+// latency where they are few: 256 requests of one token 6 us, three round trips to memory (offsets
+// and lengths; the rows and the table's entry; the old scale) and the writes.
 //
-// Read.  Units of consecutive rows of one request; 8 codes in, 8 values out per thread and step.
+// Read.  Units of four consecutive rows of one request; each thread widens the codes of 16
+// bytes of output, which a wave's stores join to whole lines.  30935 rows as fp32 (63 MB in, 253
+// out) 55 us, 5.8 TB/s; as bf16 51 us for 49385 rows, 5.9 TB/s; with 8 codes to a thread also in
+// fp32 66 us, with units of 16 rows 76, with stores past the caches 132.
 #include "kda_attn_q8.hpp"
 
 namespace kda {
 namespace {
 
 // 8 values of a row.
-template <typename E> struct Eight;
 template <typename E> struct Eight;
 template <> struct Eight<float> {
   float4 a, b;
@@ -211,9 +217,7 @@ template <typename E, int CODE> struct Out {
   }
 };
 
-// Rows of a unit: few, so that even a small call has a few loads per thread and many units
-// (33000 rows as fp32: 66 us with 4 rows, 76 with 16, 81 with 32; stores that bypass the
-// caches 132).
+// Rows of a unit: few, so that a small call has many units and few loads per thread.
 constexpr int READ_ROWS = 4;
 
 template <typename E, int DIM, int CODE>
@@ -280,6 +284,7 @@ template <typename E, int DIM, int CODE> hipError_t append_go(const CacheQ8Launc
   const uint32_t items = (uint32_t)L.total / L.block.d + 2u * (uint32_t)L.n;
   const uint32_t units = items * (uint32_t)L.hkv;
   const hipStream_t stream = (hipStream_t)L.stream;
+  // as many waves as hold a block's rows (128 channels) in their registers, four at most
   if (L.block.d <= 16)
     hipLaunchKernelGGL((append_q8_kernel<E, DIM, CODE, 1>), dim3((units + 3) / 4), dim3(256), 0, stream, L, units);
   else if (L.block.d <= 32)

@@ -2,15 +2,23 @@
 //
 // The one-pass softmax of the 16-bit rows kernel: a workgroup of four waves holds 16 or 32
 // rows of one kv head, each wave walks its own quarter of the keys, and the four are joined
-// through LDS at the end.  Codes come by DMA into each wave's own LDS double buffer as
-// they are, 32 keys at a time with their scales, and are widened in registers right
-// before the matrix instructions: a key's codes are widened once for all rows.
+// through LDS at the end.  Codes come by DMA into each wave's own part of LDS as they are, 32
+// keys at a time with their scales, and are widened in registers right before the matrix
+// instructions, once for all rows:
 //
 //   scores   a lane's 16 bytes are 16 channels of one key: two fragments, widened with the
 //            key's scale (a power of two, so the values are exact in bf16)
 //   values   the transposing 8-byte read gives a lane 8 keys of one channel; the keys'
-//            scales go into the probabilities, which are rounded to bf16 (for fp16 rows
-//            to a pair of bf16, 16 bits: bf16 has the range that a scale may ask for)
+//            scales go into the probabilities, which become bf16 (whatever the rows' type: it has
+//            the range that a scale may ask for), as a pair where that is free or needed
+//
+// Bound by HBM: a key's codes are 256 bytes for 128 channels, half of the 16-bit cache's, and are
+// read once for all rows of the tile.  256 ragged decode requests (0.86 GB of codes): 166 to 171
+// us, 5.0 to 5.2 TB/s (with even lengths of 4096 keys 5.4), where a large copy reaches 5.2 and a
+// plain read 6.3.  The same DMA with nothing computed takes 2 to 4 % less, so what is left is the
+// ragged end and the start of a short stream.  One buffer each for K and V, refilled as soon as it
+// is read, leaves room for four workgroups on a compute unit; a double buffer and two workgroups
+// take the same time, as do all heads of a piece on one XCD.
 #include "kda_attn_q8.hpp"
 
 namespace kda {
@@ -62,7 +70,10 @@ template <typename E, int DIM, int RB, int CODE>
 __global__ __launch_bounds__(256, RB == 1 ? 4 : 2) void rows_q8_kernel(const AttnQ8Launch a) {
   typedef typename Half<E>::frag frag;
   constexpr uint32_t ALL = ~0u;
-  constexpr bool PAIR = std::is_same_v<E, _Float16>;  // probabilities as a pair of bf16
+  // Probabilities as a pair of bf16: 16 bits.  With 16 rows the second product is free (256 requests of
+  // 64 .. 8192 keys: 179 us with and without), with 32 it takes time (8 tokens each: 264 us, 248 us
+  // without), and rows in fp16 need its bits.
+  constexpr bool PAIR = RB == 1 || std::is_same_v<E, _Float16>;
   constexpr int P = DIM / 16;                    // 16-byte pieces per row
   constexpr int NI = KT * P / 64;                // DMA instructions per K or V tile
   constexpr int QS = DIM / 32;                   // fragments of a row
@@ -76,7 +87,7 @@ __global__ __launch_bounds__(256, RB == 1 ? 4 : 2) void rows_q8_kernel(const Att
 
   const int lane = threadIdx.x & 63, wave = wave_of();
   const int l16 = lane & 15, gq = lane >> 4;
-  // heads fastest, so that neighbouring workgroups share pages
+  // heads fastest, so that neighbouring workgroups share pages of the table and lines of the scales
   const uint32_t unit = fdiv(blockIdx.x, a.hdiv);
   const int kvh = (int)(blockIdx.x - unit * a.hkv), split = blockIdx.y;
   const RowTile rt = request_tile(a, (int)unit);

@@ -1,4 +1,5 @@
-// Paged attention of long chunks of new tokens (bf16, fp16).
+// Paged attention of long chunks of new tokens (bf16, fp16), over a cache of that type or in
+// 8 bits: the kernel that both instantiate.
 //
 // The same one-pass softmax as the rows kernel, with the work of a matrix product:
 // a workgroup holds 32 rows per wave and all its waves walk the keys together, 64
@@ -28,6 +29,20 @@
 // two workgroups of four waves (128 rows, a tile a barrier) even out ragged requests
 // (33 requests of 1 .. 700 tokens: 157 us against 184 us; 2048 tokens on 131072 keys:
 // 4.54 ms against 3.93 ms, both without splits).
+//
+// Over a cache in 8 bits the products are the same: each tile's codes are widened once for the
+// workgroup's rows, with their scales, into the tile in LDS that a 16-bit cache's DMA would fill.
+// 2048 tokens on 131072 keys, 32 heads on 8, take 3.96 to 4.08 ms in e4m3 and 4.2 to 4.4 in int8
+// (five conversions for two int8 codes, one for two of e4m3), 5 to 8 % and 12 to 16 % more than
+// in 16 bits on the same card: the conversions and addresses are vector and scalar work of
+// the same waves (without either: 3.5 ms).  Measured on the way, e4m3:
+//   codes fetched and widened at the end of two tiles, by flat loads          4.74 ms
+//   by global loads (every LDS read waits for a flat load)                    4.59 ms
+//   fragment reads and products in an order spelled out                       4.18 ms
+//   one tile's codes in registers, widened among the scores' products,
+//   fetched among the values'                                                 4.08 ms
+//   the fetch without branches                                                4.05 ms
+//   nothing to spread the writes over all banks, writes two products later    3.96 ms
 #pragma once
 #include "kda_attn_q8.hpp"
 

@@ -4,6 +4,10 @@
 // turns and brought to half a turn either way, so that far positions lose nothing; its
 // sine and cosine are fp32.  A workgroup computes the sines and cosines of a few tokens
 // once, in LDS, and then streams the tokens' heads past them.
+//
+// Bound by HBM where tokens are many: 32768 of 40 heads of 128 fp16 channels (336 MB in and
+// out) 127 us, 5.3 TB/s, where a large copy reaches 5.2; by latency where they are few (256
+// tokens 3.6 us), so few tokens have a workgroup each, many share one by four.
 #include <math.h>
 
 #include <cmath>
@@ -214,6 +218,8 @@ KDA_API kda_status kda_rotary(const kda_rotary_args* a) {
   L.turns = !wide ? a->pairs : inter ? 2 * a->pairs / V : a->pairs / V;
   const int pass = q_here && (k_here || !has_k) ? 0 : (a->head_dim - 2 * a->pairs) / (wide ? V : 1);
   L.units = L.turns + pass;
+  // Tokens that share a workgroup: 32768 of 40 heads 127 us by four, 132 us one by one; 4096 the
+  // same either way, 2048 13.0 and 9.8 us, 256 4.6 and 3.4 us.
   L.tb = T >= 4096 ? MAX_TB : 1;
   L.by_units = fast_div((uint32_t)L.units);
   L.by_heads = fast_div((uint32_t)L.heads);
