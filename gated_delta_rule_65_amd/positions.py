@@ -58,7 +58,8 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
                 frequency, the slowest one is divided by factor
       "turns"   pairs that make fast_turns turns and more over original_length positions keep theirs,
                 those of slow_turns and fewer are divided by factor, with a ramp over the
-                pair index between (the `scale` of rotary is then usually 0.1 ln(factor) + 1)
+                pair index between, its ends rounded outward to whole pairs from the first one
+                on (the `scale` of rotary is then usually 0.1 ln(factor) + 1)
     """
     rotary_dim = int(rotary_dim)
     if rotary_dim < 2 or rotary_dim % 2:
@@ -80,14 +81,14 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
             _fail('scaling "turns" needs original_length > 0')
         if not (0 < slow_turns < fast_turns):
             _fail("turns must satisfy 0 < slow_turns < fast_turns")
-        if base == 1.0:
-            _fail('scaling "turns" needs a base other than 1')
+        if base <= 1.0:
+            _fail('scaling "turns" needs a base above 1')
 
         def index(turns):       # of the pair that makes this many turns
             return rotary_dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
 
-        lo = min(max(math.floor(index(fast_turns)), 0), rotary_dim // 2 - 1)
-        hi = min(max(math.ceil(index(slow_turns)), 0), rotary_dim // 2 - 1)
+        lo = max(math.floor(index(fast_turns)), 0)
+        hi = max(math.ceil(index(slow_turns)), 0)
         slow = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
         f = f * (1 - slow) + f / factor * slow
     elif scaling not in (None, "base"):

@@ -134,12 +134,28 @@ def test_frequencies_follow_their_formulas():
         assert torch.allclose(R.rotary_frequencies(64, scaling=s, original_length=4096), f, rtol=1e-14)
 
 
+def test_pairs_of_many_turns_are_not_divided_in_full():
+    # 32 channels over 10^6 positions: every pair makes more than a turn (the slowest 28), so
+    # none is divided by the whole factor, and the ramp runs from 32 turns (pair 14.8) to 1 (pair 20.8)
+    plain = R.rotary_frequencies(32)
+    t = R.rotary_frequencies(32, scaling="turns", factor=8.0, original_length=10 ** 6)
+    assert torch.equal(t[:15], plain[:15])
+    slow = (15 - 14) / (21 - 14)        # of the last pair, the ends rounded outward
+    assert float(t[15]) == pytest.approx(float(plain[15]) * (1 - slow + slow / 8), rel=1e-12)
+    # over 10 positions no pair makes 32 turns: the ramp starts at the first pair
+    t = R.rotary_frequencies(32, scaling="turns", factor=8.0, original_length=10)
+    # and ends at pair 0.8, rounded up
+    assert t[0] == plain[0]
+    assert torch.allclose(t[1:], plain[1:] / 8, rtol=1e-14)
+
+
 @pytest.mark.parametrize("a,kw", [
     ((63,), {}), ((0,), {}), ((64,), dict(base=-1.0)), ((64,), dict(base=float("inf"))),
     ((64,), dict(factor=0.0)), ((64,), dict(scaling="other")), ((2,), dict(scaling="base", factor=2.0)),
     ((64,), dict(scaling="turns", factor=2.0)), ((64,), dict(scaling="turns", original_length=0)),
     ((64,), dict(scaling="turns", original_length=100, slow_turns=3, fast_turns=2)),
     ((64,), dict(scaling="turns", original_length=100, base=1.0)),
+    ((64,), dict(scaling="turns", original_length=100, base=0.5)),
 ])
 def test_frequencies_refuse(a, kw):
     with pytest.raises(ValueError):
