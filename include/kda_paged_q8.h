@@ -27,7 +27,7 @@
  * host-side checks, streams and reentrancy are those of kda.h: nothing is allocated,
  * nothing is queued or written on an error, work is queued on `stream`, and values in
  * device memory are the caller's contract.  Whatever they hold, no kernel reads or writes
- * outside the buffers described by the arguments.
+ * outside the buffers described by the arguments.  Outputs share no memory with inputs or one another.
  */
 #ifndef KDA_PAGED_Q8_H_
 #define KDA_PAGED_Q8_H_
@@ -115,8 +115,11 @@ kda_status kda_kv_read_q8(const kda_kv_read_q8_args *a);
  * stands for: the same rows, masks, splits, workspace and guarantees, with q and out in
  * bf16 or fp16 (a check in fp32 reads the cache back and attends over that).
  *
- * In fp16 the values are rounded to fp16 first, which changes only those below its normal
- * numbers; magnitudes stay below 65520 there.  What a hidden position's codes and its
+ * The values' magnitudes stay below 2^99 (rows in fp16: 65520).  In fp16 the values are rounded to
+ * fp16 first, which changes only those below its normal numbers.  Scores, sums and softmax statistics
+ * are fp32.  Probabilities are rounded to q's type, or, where a request has up to 32 rows per kv head,
+ * to bf16 after the product with V's scale: as a pair of bf16 (16 bits) up to 16 rows and in
+ * fp16.  What a hidden position's codes and its
  * block's scale hold does not reach a row that does not see it.  Scales are read by their exponent:
  * one that is not a power of two counts as the next below.
  *
