@@ -168,6 +168,18 @@ kda_status check_attention(const kda_paged_attention_args* a, kda::AttnLaunch& L
     // requests: 93 us with 1024 keys, 108 us with 2048; 512 tokens alone: 59 and 80 us)
     L.min_keys = units + (int64_t)a->n * a->hkv >= 2048 ? 2048 : units >= 256 ? 1024 : 512;
     grid = units >= (L.tile_waves == 8 ? 256 : 512) * (a->n > 1 ? 3 : 1) ? 0 : units >= 256 ? 8192 : 1024;
+    // Over a cache in 8 bits several requests are cut up to a finer grid, into longer pieces
+    // where rows are many.  24 requests of 64 .. 1000 tokens on 1 .. 8000 keys (32 heads on 8, 128
+    // channels): 468 us uncut as by the rules above, 436, 416 and 402 us in pieces of 1024, 1536 and
+    // 2048 keys; 8 of 100 .. 2000 tokens 367, 290, 275 and 273 us, of 16 heads on 16 172 us by
+    // those rules, 169, 156 and 179 us, of 64 channels 241, 179, 161 and 167 us; 24 on up to 33000
+    // keys (eight waves) 1628, 1243, 1227 and 1178 us.  255 decodes beside 512 tokens: 122 us with
+    // 1024 keys, 145 us with 2048.  Even requests would like to stay whole (8 of 512 tokens on
+    // 4000 keys: 305 us, 349 us with 1536, 400 us with 1024), but nothing here tells them.
+    if (cache_bytes == 1) {
+      L.min_keys = L.tile_waves == 8 ? 2048 : units >= 256 ? 1536 : units + (int64_t)a->n * a->hkv >= 2048 ? 1024 : 512;
+      if (a->n > 1 && units >= 256) grid = 8192;
+    }
   } else {
     // chunks: 64 keys at least.  With 32, 64, 96, 128 and 256 keys 3 chunks of 840 tokens take
     // 51, 41, 48, 58 and 75 us, 300 tokens on 700 keys 27, 24, 31, 34 and 63 us, 4 fresh
