@@ -327,6 +327,26 @@ def test_tiles_of_eight_waves(code, dim, dt):
             assert np.all(np.abs(lse[x].double().numpy() - rl[x]) <= tl[x]), x
 
 
+@pytest.mark.parametrize("dim,dt,cols", [(128, BF, 0), (64, HF, 0), (128, BF, 520)])
+@pytest.mark.parametrize("code", CODES)
+def test_ragged_requests_cut_into_pieces(code, dim, dt, cols):
+    # rows for 256 workgroups and keys for two pieces; a wide table's take eight waves and more pieces
+    c, cache = Q.make([3600, 60, 1700], [500, 90, 500], 32, 8, dim, 64, 32, dt, code, seed=6, pad_rows=2)
+    if cols:
+        table = torch.full((3, cols), -1, dtype=torch.int32)
+        table[:, :c.table.shape[1]] = c.table
+        c.table = table
+    nbytes = P8.paged_attention_q8_workspace_bytes(c.q.to(DEV), *cache.tensors(DEV), c.table.to(DEV))
+    assert nbytes > 0       # it is cut
+    rows = {0, 63, 255, 499, 500, 589, 590, 811, 1089}
+    out, lse = attend(c, cache)
+    ref, rl, tol, tl = R.attention(c, cache.page, dim ** -0.5, rows=rows)
+    for x in rows:
+        assert np.all(np.abs(out[x].double().numpy() - ref[x]) <= tol[x]), x
+        assert np.all(np.abs(lse[x].double().numpy() - rl[x]) <= tl[x]), x
+    assert torch.all(out[1090:] == 7.0) and torch.all(lse[1090:] == 7.0)
+
+
 @pytest.mark.parametrize("dt", [BF, HF])
 @pytest.mark.parametrize("ctx,new,window,sinks", [
     (40, 3, 0, 0), (40, 30, 0, 0), (100, 90, 24, 3), (300, 200, 0, 0), (0, 300, 70, 5), (90, 6, 20, 3)])
