@@ -54,7 +54,8 @@ __device__ __forceinline__ u32x2v_t lds_read_tr8(uint32_t at) {
 // A NaN code of V spoils the product of its tile also for rows that do not see its key (0 times
 // NaN).  Where a sum is not finite, the keys are gone through twice more: once with NaN codes
 // as ones and the others as zeros, each visible key weighing one, which finds the sums that a NaN
-// belongs to, and once with zeros for NaN.
+// belongs to, and once with zeros for NaN.  The counts are never rescaled: a maximum that grows by
+// 2^150 would make them 0, where the NaN itself stays.
 enum { PLAIN = 0, COUNT = 1, ZEROED = 2 };
 __device__ __forceinline__ uint32_t without_nan(uint32_t w, int mode) {
   const uint32_t nan = (((w & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u) * 0xffu;  // bytes 0x7f, 0xff
@@ -253,7 +254,7 @@ __global__ __launch_bounds__(256, RB == 1 ? 4 : 2) void rows_q8_kernel(const Att
         mx[b] = max_quarter(x) * c;  // c > 0
         grew |= mx[b] > m[b] + LAG;
       }
-      if (__any(grew)) {
+      if (!(CODE == E4M3 && mode == COUNT) && __any(grew)) {
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
           const float nm = fmaxf(m[b], mx[b]);

@@ -605,3 +605,26 @@ def test_captured_steps_replay_as_the_eager_ones():
             torch.cuda.synchronize()
             for a, b in zip(outs + cache + [table], eager[4] + eager[1] + [eager[2]]):
                 assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("new", [1, 3, 6, 100])
+@pytest.mark.parametrize("ctx,window,sinks", [(300, 0, 0), (420, 200, 80)])
+def test_a_seen_nan_outlives_far_larger_scores(dt, new, ctx, window, sinks):
+    """A NaN code of V at an early key that every row sees, and keys behind it, of the same wave, whose scores
+    are hundreds above: one token, drafts of up to 16 and up to 32 rows, and chunks agree that it is seen."""
+    c, cache = Q.make([ctx], [new], 8, 2, 128, 16, 8, dt, "e4m3", seed=21)
+    big = 64            # keys 64 .. 71, a block, have K values 2^8 times as large
+    cache.scales[0][int(c.table[0, big // 16]), :, big % 16 // 8] *= 256.0
+    c.keys[0][big:big + 8] *= 256.0
+    for pos in (5, ctx + new - 1):      # seen by all rows, and by the last token's alone
+        cache.codes[1][int(c.table[0, pos // 16]), 0, pos % 16, 7] = 0x7f
+        c.values[0][pos, 0, 7] = float("nan")
+    out, _ = attend(c, cache, window, sinks)
+    with np.errstate(all="ignore"):
+        ref, _, tol, _ = R.attention(c, 16, 128 ** -0.5, window, sinks)
+    o = out.double().numpy()
+    fine = np.isfinite(ref)
+    assert np.array_equal(np.argwhere(~fine)[:, 2], np.full(new * 4, 7))    # the four heads on K head 0
+    assert np.array_equal(np.isfinite(o), fine)
+    assert np.all(np.abs(o[fine] - ref[fine]) <= tol[fine])
