@@ -46,6 +46,13 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2v_t __attribute__((ext_vector_type(2)));
 
+// A block's scale as it was loaded: the power of two of its exponent, sign and lower bits dropped.  e4m3's
+// conversion reads scales so by itself; everything else that takes one goes through here, so that
+// a scale that is no power of two stands for the same values in every operator.
+__device__ __forceinline__ float pow2_scale(float s) {
+  return __uint_as_float(__float_as_uint(s) & 0x7f800000u);
+}
+
 // The four codes of a word.
 template <int CODE> struct Code;
 template <> struct Code<E4M3> {
@@ -86,7 +93,7 @@ template <> struct Code<INT8> {
   // makes 1152 + b, and (1152 + b) s - 1152 s is one instruction that takes its fp16 operand
   // as it is.  Every step is exact (1152 s is a number: values lie below 2^99).  By conversions
   // of bytes to fp32 it was 11 instructions for four codes in place of 9: 2048 tokens on 131072
-  // keys 4.13 ms, now 3.94; 24 ragged prompts 895 us, now 881.
+  // keys 4.13 ms, now 3.94; 24 ragged prompts 895 us, now 881.  s is a power of two (pow2_scale).
   template <typename E> static __device__ __forceinline__ u32x2v_t widen16(E, uint32_t w, float s) {
     const uint32_t u = w ^ 0x80808080u;
     const f16x2_t a = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u));

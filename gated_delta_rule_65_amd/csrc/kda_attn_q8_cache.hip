@@ -65,6 +65,12 @@ __device__ __forceinline__ float max_wave(float x) {
   return x;
 }
 
+// The scale of a block that has rows; one that is no finite number becomes NaN, which is neither the larger
+// of two nor less than another.
+__device__ __forceinline__ float begun_scale(float s) {
+  return fabsf(s) < __builtin_inff() ? pow2_scale(s) : __builtin_nanf("");
+}
+
 // WAVES: waves that share a block.
 template <typename E, int DIM, int CODE, int WAVES>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void append_q8_kernel(const CacheQ8Launch a, uint32_t units) {
@@ -113,7 +119,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void append_q8_kerne
   uint8_t* const kc = (uint8_t*)a.kc + id * a.k_page + row_at;
   uint8_t* const vc = (uint8_t*)a.vc + id * a.v_page + row_at;
   const int64_t sc = ((int64_t)id * a.hkv + head) * a.per_page + fdiv(off, a.block);
-  const float ks0 = held > 0 ? a.ks[sc] : 0.0f, vs0 = held > 0 ? a.vs[sc] : 0.0f;
+  const float ks0 = held > 0 ? begun_scale(a.ks[sc]) : 0.0f, vs0 = held > 0 ? begun_scale(a.vs[sc]) : 0.0f;
   float ktop = 0.0f, vtop = 0.0f;
   for (int r0 = 0; r0 < rows; r0 += HOLD * RPL) {
     if (r0 > 0) load(r0);
@@ -198,13 +204,16 @@ template <typename E, int CODE> struct Out {
     s = 0.0f;
   }
   __device__ __forceinline__ void store(E* p) const {
+    float z = s;
+    asm volatile("" : "+v"(z));  // or the mask moves to the load and waits for it there: 53 us for 50
+    z = pow2_scale(z);
     float x[N];
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
       float y[4];
       Code<CODE>::widen(u[i], y);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[4 * i + j] = y[j] * s;
+      for (int j = 0; j < 4; ++j) x[4 * i + j] = y[j] * z;
     }
     if constexpr (N == 4) {
       store4(p, x[0], x[1], x[2], x[3]);

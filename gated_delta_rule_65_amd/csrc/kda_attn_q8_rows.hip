@@ -208,7 +208,8 @@ __global__ __launch_bounds__(256, RB == 1 ? 4 : 2) void rows_q8_kernel(const Att
       asm volatile("" : "+v"(at));  // or every step would keep its address
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float sk = lds_read4(sa + 256 * slot + 64 * k + 4 * l16);
+        float sk = lds_read4(sa + 256 * slot + 64 * k + 4 * l16);
+        if constexpr (CODE == INT8) sk = pow2_scale(sk);
 #pragma unroll
         for (int b = 0; b < RB; ++b) s[k][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -291,14 +292,14 @@ __global__ __launch_bounds__(256, RB == 1 ? 4 : 2) void rows_q8_kernel(const Att
 #pragma unroll
           for (int b = 0; b < RB; ++b)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s[k][b][r] = s[k][b][r] == 0.0f ? 0.0f : s[k][b][r] * vs[k][r];
+            for (int r = 0; r < 4; ++r) s[k][b][r] = s[k][b][r] == 0.0f ? 0.0f : s[k][b][r] * pow2_scale(vs[k][r]);
       } else {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int b = 0; b < RB; ++b)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s[k][b][r] *= vs[k][r];
+            for (int r = 0; r < 4; ++r) s[k][b][r] *= pow2_scale(vs[k][r]);
       }
       values();
       if (CODE == E4M3 && mode != PLAIN) {

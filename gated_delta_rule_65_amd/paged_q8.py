@@ -142,7 +142,8 @@ def kv_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqle
 
     A block's scale is the least power of two with which its rows are codes; rows that
     join earlier ones keep the scale or raise it, and the earlier codes are then rounded to it.
-    The scales of blocks that have no rows yet need no initial value.  k and v (bf16, fp16 or fp32)
+    The scales of blocks that have no rows yet need no initial value.  Scales written elsewhere have to be
+    powers of two too: any other counts as the next one below, here and in every reader.  k and v (bf16, fp16 or fp32)
     may be views of a fused projection."""
     shape, dtype = k.shape, k.dtype
     if len(shape) != 3:

@@ -16,7 +16,10 @@
  *   KDA_INT8  c is the signed number, -127 .. 127
  *
  * Scales are powers of two, 2^-126 at least: a division by one is exact, so that the code is the only
- * rounding, and every value of the cache (4 or 7 significant bits) is a bf16 number.
+ * rounding, and every value of the cache (4 or 7 significant bits) is a bf16 number.  All three
+ * read a scale by its exponent: one that is no power of two (from elsewhere, as the largest magnitude
+ * over 448) counts as the next power of two below, and an append that adds rows to its block
+ * leaves a power of two there.
  *
  * All three address rows alike: request i owns rows [cu_seqlens[i], cu_seqlens[i+1]),
  * its newest positions: row x is at position p = seq_lens[i] - (rows of i) + (x - first row of i),
@@ -53,7 +56,8 @@ typedef enum kda_code {
  *
  *   the block's first position is among the rows:  scale = need
  *   otherwise:  scale = max(scale, need), and where that is more, the codes at the
- *               block's earlier positions are rounded to it
+ *               block's earlier positions are rounded to it (a scale there that is no finite
+ *               number counts for nothing: scale = need)
  *
  * and the rows' codes are their values over the scale, rounded to nearest, ties to even.
  * NaN and infinities have no part in `need`: e4m3 holds NaN for them, int8 0 for NaN and
@@ -120,8 +124,7 @@ kda_status kda_kv_read_q8(const kda_kv_read_q8_args *a);
  * are fp32.  Probabilities are rounded to q's type, or, where a request has up to 32 rows per kv head,
  * to bf16 after the product with V's scale: as a pair of bf16 (16 bits) up to 16 rows and in
  * fp16.  What a hidden position's codes and its
- * block's scale hold does not reach a row that does not see it.  Scales are read by their exponent:
- * one that is not a power of two counts as the next below.
+ * block's scale hold does not reach a row that does not see it.
  *
  * Errors: as kda_paged_attention, and KDA_ERR_DTYPE for fp32 or an unknown code.
  */

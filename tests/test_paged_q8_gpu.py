@@ -628,3 +628,101 @@ def test_a_seen_nan_outlives_far_larger_scores(dt, new, ctx, window, sinks):
     assert np.array_equal(np.argwhere(~fine)[:, 2], np.full(new * 4, 7))    # the four heads on K head 0
     assert np.array_equal(np.isfinite(o), fine)
     assert np.all(np.abs(o[fine] - ref[fine]) <= tol[fine])
+
+
+# In [1, 2), the number before 2 among them: a scale times one has the same exponent.
+WITHIN = torch.tensor([1.0, 1.25, 1.5, 2.0 - 2.0 ** -23])
+
+
+def within(scales, seed):
+    """Scales that are not powers of two, with the exponents of these."""
+    g = torch.Generator().manual_seed(seed)
+    return scales * WITHIN[torch.randint(0, 4, scales.shape, generator=g)].to(scales.device)
+
+
+def exponents(scales):
+    return scales.cpu().view(torch.int32) & 0x7f800000
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dim,dt", [(128, BF), (64, HF)])
+@pytest.mark.parametrize("new", [1, 3, 7, 90])
+def test_scales_count_by_their_exponents_in_attention(code, dim, dt, new):
+    """Scales that are not powers of two give, bit by bit, what the powers of two below them give: over K
+    and V, in a single token, short drafts, 28 rows and chunks."""
+    c, cache = Q.make([200, 31], [new, new], 8, 2, dim, 16, 4, dt, code, seed=30 + new)
+    kc, vc, ks, vs = cache.tensors(DEV)
+    args = c.table.to(DEV), c.cu.to(DEV), c.seq.to(DEV)
+    print("exponents", code, dim, dt, new, flush=True)
+    for odd_k, odd_v in ((True, False), (False, True)):
+        o = P8.paged_attention_q8(c.q.to(DEV), kc, vc, within(ks, 1) if odd_k else ks, within(vs, 2) if odd_v else vs,
+                                  *args, return_lse=True, max_new_len=new)
+        p = P8.paged_attention_q8(c.q.to(DEV), kc, vc, ks, vs, *args, return_lse=True, max_new_len=new)
+        torch.cuda.synchronize()
+        assert torch.equal(o[0], p[0]) and torch.equal(o[1], p[1]), (odd_k, odd_v)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dt", [BF, HF, FP])
+def test_scales_count_by_their_exponents_in_reads(code, dt):
+    c, cache = Q.make([70, 9], [1, 1], 2, 2, 64, 16, 4, dt, code, seed=40)
+    kc, vc, ks, vs = cache.tensors(DEV)
+    cu = i32([0] + list(np.cumsum(c.seq.tolist())))
+    print("exponents", code, dt, flush=True)
+    got = [P8.kv_read_q8(kc, vc, *s, c.table.to(DEV), cu, c.seq.to(DEV), total_tokens=int(cu[-1]), dtype=dt)
+           for s in ((ks, vs), (within(ks, 3), within(vs, 4)))]
+    torch.cuda.synchronize()
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("page,block", [(16, 4), (48, 24), (128, 128)])
+def test_scales_count_by_their_exponents_in_appends(code, page, block):
+    """Rows that join a block keep the power of two or raise it, and leave a power of two there; blocks
+    without new rows keep what they hold."""
+    ctx, n = [70, 9, 33], 3
+    c, cache = Q.make(ctx, [2] * n, 2, 2, 64, page, block, BF, code, seed=50)
+    plain = cache.tensors(DEV)
+    odd = [t.clone() for t in plain[:2]] + [within(s, i) for i, s in enumerate(plain[2:])]
+    before = [s.clone() for s in odd[2:]]
+    touched = torch.zeros(plain[2].shape, dtype=torch.bool)
+    for i, t in enumerate(ctx):
+        for p in (t, t + 1):
+            touched[int(c.table[i, p // page]), :, p % page // block] = True
+    g = torch.Generator().manual_seed(6)
+    k, v = (torch.randn(2 * n, 2, 64, generator=g) for _ in range(2))
+    k[2:] *= 1e-3                   # scales that stay
+    v[:4] *= 1e3                    # and scales that grow
+    k, v = k.to(BF).to(DEV), v.to(BF).to(DEV)
+    print("exponents", code, page, block, flush=True)
+    for cache in (plain, odd):
+        P8.kv_append_q8(k, v, *cache, c.table.to(DEV), c.cu.to(DEV), c.seq.to(DEV))
+    torch.cuda.synchronize()
+    for side in (0, 1):
+        assert torch.equal(plain[side].view(torch.uint8), odd[side].view(torch.uint8))
+        p, o = plain[2 + side].cpu(), odd[2 + side].cpu()
+        assert torch.equal(p[touched], o[touched])
+        assert torch.equal(o[~touched].view(torch.int32), before[side].cpu()[~touched].view(torch.int32))
+        assert torch.equal(exponents(o), exponents(p))
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
+def test_a_begun_block_without_a_scale_takes_the_rows(code, what):
+    """Rows that start inside a block whose memory nobody has set: the scale is theirs."""
+    page, block, hkv, dim = 16, 8, 2, 64
+    g = torch.Generator().manual_seed(7)
+    k, v = (torch.randn(3, hkv, dim, generator=g).to(BF) for _ in range(2))
+    table, cu, seq = torch.tensor([[1, 0]], dtype=torch.int32), [0, 3], [6]
+    cache = Q.Cache(2, hkv, page, dim, block, code, scale=1.0)
+    dev = cache.tensors(DEV)
+    for side in (0, 1):
+        dev[2 + side][1, :, 0] = what
+        cache.scales[side][1, :, 0] = 0.0       # below any that the rows need
+        cache.codes[side][1, :, :3] = 0         # and rounded to zeros by it here
+        dev[side].view(torch.uint8)[1, :, :3] = 0
+    print("no scale", code, what, flush=True)
+    P8.kv_append_q8(k.to(DEV), v.to(DEV), *dev, table.to(DEV), i32(cu), i32(seq))
+    torch.cuda.synchronize()
+    cache.append(k, v, table, cu, seq)
+    assert cache.same(dev)
