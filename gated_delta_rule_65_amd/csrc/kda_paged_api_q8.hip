@@ -6,7 +6,8 @@
 
 namespace {
 
-constexpr int64_t MAX_UNITS = (int64_t)1 << 24;  // workgroups of a call that moves rows
+// Workgroups of a call that moves rows: up to 256 threads each, and a launch holds fewer than 2^32.
+constexpr int64_t MAX_UNITS = ((int64_t)1 << 24) - 1;
 
 kda_status check_codes(int code, int page_size, int block) {
   if (code != KDA_E4M3 && code != KDA_INT8) FAIL(KDA_ERR_DTYPE, "unknown code %d", code);
@@ -102,8 +103,8 @@ KDA_API kda_status kda_kv_append_q8(const kda_kv_append_q8_args* a) {
   kda::CacheQ8Launch L = {};
   kda_status s = check_rows(a, L);
   if (s != KDA_OK) return s;
-  if ((a->total_tokens / a->block + 2 * (int64_t)a->n) > MAX_UNITS / a->hkv)
-    FAIL(KDA_ERR_UNSUPPORTED, "blocks of rows, over the heads, above 2^24");
+  if ((a->total_tokens / a->block + 2 * (int64_t)a->n) * a->hkv > MAX_UNITS)
+    FAIL(KDA_ERR_UNSUPPORTED, "blocks of rows, over the heads, not below 2^24");
   const size_t es = elem_size(a->dtype);
   const int64_t dense = (int64_t)a->hkv * a->head_dim;
   int64_t ks, vs;
@@ -129,7 +130,7 @@ KDA_API kda_status kda_kv_read_q8(const kda_kv_read_q8_args* a) {
   kda_status s = check_rows(a, L);
   if (s != KDA_OK) return s;
   if (a->total_tokens / 4 + a->n > MAX_UNITS)
-    FAIL(KDA_ERR_UNSUPPORTED, "total_tokens above 2^26, or requests near 2^24");
+    FAIL(KDA_ERR_UNSUPPORTED, "total_tokens near 2^26, or requests near 2^24");
   if (misaligned({a->k_out, a->v_out}, 16))
     FAIL(KDA_ERR_ARG, "tensor base pointers must be 16-byte aligned");
   if (a->n == 0 || a->total_tokens == 0) return (kda_status)kda::set_ok();

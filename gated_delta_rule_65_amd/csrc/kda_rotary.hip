@@ -23,6 +23,7 @@ namespace kda {
 namespace {
 
 constexpr int MAX_DIM = 512, MAX_TB = 4;
+constexpr int64_t MAX_GROUPS = ((int64_t)1 << 24) - 1;  // of 256: a launch holds fewer than 2^32 threads
 
 struct RotaryLaunch {
   const void *q, *k;
@@ -188,6 +189,11 @@ KDA_API kda_status kda_rotary(const kda_rotary_args* a) {
   }
   if (a->total_tokens > (int64_t)INT32_MAX / ((a->hq + hk) * a->head_dim * es / 16))
     FAIL(KDA_ERR_UNSUPPORTED, "total_tokens * heads * head_dim above 2^31-1 16-byte pieces");
+  // Tokens that share a workgroup: 32768 of 40 heads 127 us by four, 132 us one by one; 4096 the
+  // same either way, 2048 13.0 and 9.8 us, 256 4.6 and 3.4 us.
+  L.tb = a->total_tokens >= 4096 ? MAX_TB : 1;
+  if ((a->total_tokens + L.tb - 1) / L.tb > MAX_GROUPS)
+    FAIL(KDA_ERR_UNSUPPORTED, "total_tokens above 2^26 - 4");
   for (const void* p : {a->q, a->k, (const void*)a->q_out, (const void*)a->k_out})
     if (reinterpret_cast<uintptr_t>(p) & 15) FAIL(KDA_ERR_ARG, "tensor base pointers must be 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(a->positions) & 3 || reinterpret_cast<uintptr_t>(a->frequencies) & 7)
@@ -218,9 +224,6 @@ KDA_API kda_status kda_rotary(const kda_rotary_args* a) {
   L.turns = !wide ? a->pairs : inter ? 2 * a->pairs / V : a->pairs / V;
   const int pass = q_here && (k_here || !has_k) ? 0 : (a->head_dim - 2 * a->pairs) / (wide ? V : 1);
   L.units = L.turns + pass;
-  // Tokens that share a workgroup: 32768 of 40 heads 127 us by four, 132 us one by one; 4096 the
-  // same either way, 2048 13.0 and 9.8 us, 256 4.6 and 3.4 us.
-  L.tb = T >= 4096 ? MAX_TB : 1;
   L.by_units = fast_div((uint32_t)L.units);
   L.by_heads = fast_div((uint32_t)L.heads);
   L.by_n = fast_div((uint32_t)L.n);

@@ -67,7 +67,7 @@ typedef enum kda_code {
  *
  * Errors: KDA_ERR_ARG (NULL, bad struct, misaligned), KDA_ERR_DTYPE (dtype, code), KDA_ERR_SHAPE,
  * KDA_ERR_UNSUPPORTED (head_dim other than 64 or 128, num_pages * page_size or max_pages *
- * page_size above 2^30, blocks of rows near 2^24 in all).
+ * page_size above 2^30, (T / block + 2 n) * Hkv not below 2^24).
  */
 typedef struct kda_kv_append_q8_args {
   size_t struct_size;          /* = sizeof(kda_kv_append_q8_args) */
@@ -94,7 +94,7 @@ kda_status kda_kv_append_q8(const kda_kv_append_q8_args *a);
  * row without a page or with a position below 0.  Rows of k_out and v_out behind the last request are
  * left as they are.  cu_seqlens of the running sums of seq_lens reads whole contexts.
  *
- * Errors: as kda_kv_append_q8.
+ * Errors: as kda_kv_append_q8, with T / 4 + n not below 2^24 in place of the blocks.
  */
 typedef struct kda_kv_read_q8_args {
   size_t struct_size;          /* = sizeof(kda_kv_read_q8_args) */

@@ -37,7 +37,7 @@ extern "C" {
  *
  * Errors: KDA_ERR_ARG (NULL, bad struct, misaligned, shared memory), KDA_ERR_DTYPE, KDA_ERR_SHAPE,
  * KDA_ERR_UNSUPPORTED (head_dim not a multiple of 8 or above 512, rows that need more than
- * 2^31 - 1 pieces of 16 bytes).
+ * 2^31 - 1 pieces of 16 bytes, more than 2^26 - 4 tokens).
  */
 typedef struct kda_rotary_args {
   size_t struct_size;          /* = sizeof(kda_rotary_args) */

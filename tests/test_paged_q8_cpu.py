@@ -244,3 +244,18 @@ def test_the_reference_rounds_as_torch_does():
     assert np.array_equal(Q.nearest(y.double().numpy(), "e4m3"), want)
     assert Q.least_scale(448.0, "e4m3") == 1 and Q.least_scale(448.1, "e4m3") == 2
     assert Q.least_scale(127.0, "int8") == 1 and Q.least_scale(0.0, "int8") == 2.0 ** -126
+
+
+# A launch holds fewer than 2^32 threads, so fewer than 2^24 workgroups of 256.
+@pytest.mark.parametrize("fields", [
+    dict(n=1, hkv=1, block=16, total_tokens=((1 << 24) - 2) * 16), dict(n=2, hkv=2, block=8, total_tokens=((1 << 23) - 4) * 8),
+    dict(n=1 << 22, hkv=2, block=16, total_tokens=1), dict(n=3, hkv=5, block=16, total_tokens=((1 << 24) // 5 + 1 - 6) * 16)])
+def test_appends_past_a_launch_are_unsupported(lib, fields):
+    assert lib.kda_kv_append_q8(ctypes.byref(append(**fields))) == UNSUP
+    assert b"2^24" in lib.kda_last_error()
+
+
+@pytest.mark.parametrize("fields", [dict(n=2, total_tokens=((1 << 24) - 2) * 4), dict(n=(1 << 24) - 1, total_tokens=4), dict(n=1 << 24, total_tokens=1)])
+def test_reads_past_a_launch_are_unsupported(lib, fields):
+    assert lib.kda_kv_read_q8(ctypes.byref(read(**fields))) == UNSUP
+    assert b"2^26" in lib.kda_last_error()

@@ -160,3 +160,12 @@ def test_pairs_of_many_turns_are_not_divided_in_full():
 def test_frequencies_refuse(a, kw):
     with pytest.raises(ValueError):
         R.rotary_frequencies(*a, **kw)
+
+
+@pytest.mark.parametrize("fields", [
+    # a launch holds fewer than 2^32 threads: workgroups of 256, four tokens each
+    dict(total_tokens=1 << 26), dict(total_tokens=(1 << 26) - 3), dict(total_tokens=1 << 28), dict(total_tokens=(1 << 26) + 1, dtype=0)])
+def test_tokens_past_a_launch_are_unsupported(lib, fields):
+    a = args(**{**dict(hq=1, hk=0, k=None, k_out=None, head_dim=8, pairs=4, q=1 << 40, q_out=1 << 50), **fields})
+    assert lib.kda_rotary(ctypes.byref(a)) == UNSUP
+    assert b"2^26" in lib.kda_last_error()
