@@ -726,3 +726,38 @@ def test_a_begun_block_without_a_scale_takes_the_rows(code, what):
     torch.cuda.synchronize()
     cache.append(k, v, table, cu, seq)
     assert cache.same(dev)
+
+
+@pytest.mark.parametrize("dim,dt", [(128, BF), (64, HF)])
+@pytest.mark.parametrize("code", CODES)
+def test_tiles_of_eight_waves_cut_into_pieces(code, dim, dt):
+    """Ragged requests whose rows fill the chip with workgroups of 256, over a wide table: eight waves, and
+    visits of two pieces and three.  (A wide table alone does not take eight waves: 1092 tokens of 32 heads on 8
+    make 144 such workgroups, and run on four.)  Over e4m3, with a NaN code too that one request's last token sees."""
+    hq, hkv, cols = 64, 8, 520
+    new = [600, 30, 430]
+    c, cache = Q.make([4500, 9, 6300], new, hq, hkv, dim, 64, 32, dt, code, seed=8, pad_rows=2)
+    table = torch.full((3, cols), -1, dtype=torch.int32)
+    table[:, :c.table.shape[1]] = c.table
+    c.table = table
+    # 272 workgroups of 256 rows; pieces of 2048 keys at least, so 16 at most in 33280 (four waves: 15)
+    rows, pieces = (sum(new) + 2) * hq, 16
+    need = pieces * rows * dim * 4 + pieces * rows * 4 + rows * 4
+    assert P8.paged_attention_q8_workspace_bytes(c.q, *cache.tensors(), c.table) == need
+    look = {0, 63, 255, 599, 600, 629, 630, 811, 1058, 1059}
+    for nan in ([False, True] if code == "e4m3" else [False]):
+        if nan:
+            pos = 4500 + 599
+            cache.codes[1][int(c.table[0, pos // 64]), 3, pos % 64, 20] = 0xff
+            c.values[0][pos, 3, 20] = float("nan")
+        out, lse = attend(c, cache)
+        with np.errstate(all="ignore"):
+            ref, rl, tol, tl = R.attention(c, 64, dim ** -0.5, rows=look)
+        o, fine = out.double().numpy(), np.isfinite(ref)
+        assert np.count_nonzero(~fine) == (8 if nan else 0)     # the last token's eight heads on K head 3
+        for x in sorted(look):
+            f = fine[x]
+            assert np.array_equal(np.isfinite(o[x]), f), x
+            assert np.all(np.abs(o[x] - ref[x])[f] <= tol[x][f]), x
+            assert np.all(np.abs(lse[x].double().numpy() - rl[x]) <= tl[x]), x
+        assert torch.all(out[1060:] == 7.0) and torch.all(lse[1060:] == 7.0)
