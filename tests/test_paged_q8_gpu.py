@@ -761,3 +761,44 @@ def test_tiles_of_eight_waves_cut_into_pieces(code, dim, dt):
             assert np.all(np.abs(o[x] - ref[x])[f] <= tol[x][f]), x
             assert np.all(np.abs(lse[x].double().numpy() - rl[x]) <= tl[x]), x
         assert torch.all(out[1060:] == 7.0) and torch.all(lse[1060:] == 7.0)
+
+
+@pytest.mark.parametrize("n", [4, 64, 300])
+@pytest.mark.parametrize("code", CODES)
+def test_offsets_out_of_order_write_nothing_else(n, code):
+    """Offsets that decrease, lie below 0 or past the rows: a block of the cache is what its request's rows make it
+    or untouched, pages of no request are untouched, and so is what lies around the rows read."""
+    page, block, hkv, dim, T = 8, 4, 2, 64, 210
+    g = torch.Generator().manual_seed(n)
+    cu = torch.sort(torch.randint(0, T + 1, (n + 1,), generator=g)).values
+    swap = torch.randperm(n + 1, generator=g)[:max(2, n // 4)]
+    cu[swap] = torch.randint(-50, T + 50, (swap.numel(),), generator=g)
+    if n == 4:
+        cu = torch.tensor([0, 40, 10, 90, T + 50])
+    seq = torch.randint(0, 2 * page + 1, (n,), generator=g)
+    pages = 4 * n
+    table = torch.randperm(pages, generator=g)[:2 * n].view(n, 2).to(torch.int32)   # half of the pages
+    k, v = (torch.randn(T, hkv, dim, generator=g).to(BF) for _ in range(2))
+    cache = Q.Cache(pages, hkv, page, dim, block, code, scale=1.0)
+    old = [x.copy() for x in cache.codes + cache.scales]
+    dev = cache.tensors(DEV)
+    print("out of order", n, code, flush=True)
+    P8.kv_append_q8(k.to(DEV), v.to(DEV), *dev, table.to(DEV), i32(cu), i32(seq))
+    torch.cuda.synchronize()
+    cache.append(k, v, table, cu.clamp(0, T).tolist(), seq.tolist())
+    shape = (pages, hkv, page // block, block * dim)
+    made = 0
+    for side in (0, 1):
+        codes, scales = dev[side].cpu().view(torch.uint8).numpy().reshape(shape), dev[2 + side].cpu().numpy()
+        is_old = (codes == old[side].reshape(shape)).all(-1) & (scales == old[2 + side])
+        is_new = (codes == cache.codes[side].reshape(shape)).all(-1) & (scales == cache.scales[side])
+        assert np.all(is_old | is_new)
+        unlisted = np.setdiff1d(np.arange(pages), table.numpy())
+        assert np.all(is_old[unlisted])
+        made += int((~is_old).sum())
+    assert made > 0
+    room = [torch.full((T + 40, hkv, dim), 9.0, device=DEV) for _ in range(2)]
+    P8.kv_read_q8(*dev, table.to(DEV), i32(cu), i32(seq), k_out=room[0][20:20 + T], v_out=room[1][20:20 + T])
+    torch.cuda.synchronize()
+    for x in room:
+        assert torch.all(x[:20] == 9.0) and torch.all(x[20 + T:] == 9.0)
