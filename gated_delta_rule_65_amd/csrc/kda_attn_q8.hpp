@@ -89,7 +89,7 @@ template <> struct Code<INT8> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)(w >> (8 * i));
   }
-  // The low byte of an fp16 number of 2^10 is its integer part: put there, the unsigned byte b + 128
+  // (A known device.)  The low byte of an fp16 number of 2^10 is its integer part: put there, the unsigned byte b + 128
   // makes 1152 + b, and (1152 + b) s - 1152 s is one instruction that takes its fp16 operand
   // as it is.  Every step is exact (1152 s is a number: values lie below 2^99).  By conversions
   // of bytes to fp32 it was 11 instructions for four codes in place of 9: 2048 tokens on 131072

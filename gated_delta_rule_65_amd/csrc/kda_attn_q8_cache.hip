@@ -7,9 +7,12 @@
 // there are no atomics, and the rows are read once.  Request i's units start at
 // floor(cu[i] / block) + 2 i, which leaves it as many as its rows can touch.  Bound by HBM
 // where rows are many: 30669 tokens of 8 heads of 128 bf16 channels (126 MB in, 63 MB out) 46 us,
-// 4.1 TB/s, in blocks of 16, 32 (one wave a block: 51 us, four: 59) or 64; by
-// latency where they are few: 256 requests of one token 6 us, three round trips to memory (offsets
-// and lengths; the rows and the table's entry; the old scale) and the writes.
+// 4.1 TB/s, in blocks of 8 (44 us), 16, 32 (one wave a block: 51 us, four: 59) or 64.  Smaller blocks
+// leave lanes idle and pay each unit's search and trips for fewer rows (blocks of 4: 56 us, a scale per token:
+// 190); in longer ones the rows past the registers are loaded twice by few units (128: 63 us, 256: 69,
+// 512: 78).  By latency where rows are few: 256 requests of one token 6 us, three round trips to memory
+// (offsets and lengths; the rows and the table's entry; the old scale) and the writes; in blocks of
+// 512 whose earlier rows are rounded anew 6 us more.
 //
 // Read.  Units of four consecutive rows of one request; each thread widens the codes of 16
 // bytes of output, which a wave's stores join to whole lines.  30935 rows as fp32 (63 MB in, 253
@@ -293,7 +296,8 @@ template <typename E, int DIM, int CODE> hipError_t append_go(const CacheQ8Launc
   const uint32_t items = (uint32_t)L.total / L.block.d + 2u * (uint32_t)L.n;
   const uint32_t units = items * (uint32_t)L.hkv;
   const hipStream_t stream = (hipStream_t)L.stream;
-  // as many waves as hold a block's rows (128 channels) in their registers, four at most
+  // as many waves as hold a block's rows (128 channels) in their registers, four at most (times of blocks of 1
+  // to 512 above)
   if (L.block.d <= 16)
     hipLaunchKernelGGL((append_q8_kernel<E, DIM, CODE, 1>), dim3((units + 3) / 4), dim3(256), 0, stream, L, units);
   else if (L.block.d <= 32)

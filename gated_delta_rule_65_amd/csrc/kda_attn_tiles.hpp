@@ -32,9 +32,9 @@
 //
 // Over a cache in 8 bits the products are the same: each tile's codes are widened once for the
 // workgroup's rows, with their scales, into the tile in LDS that a 16-bit cache's DMA would fill.
-// 2048 tokens on 131072 keys, 32 heads on 8, take 3.90 to 4.08 ms in e4m3 and 3.94 in int8 beside 3.90
-// (nine instructions for four int8 codes, two for four of e4m3), 5 to 8 % more than in 16 bits
-// on the same card: the conversions and addresses are vector and scalar work of
+// 2048 tokens on 131072 keys, 32 heads on 8, take 3.90 to 4.39 ms in e4m3 from card to card, and 2 to 3 %
+// more in int8 (4.03 beside 3.95: nine instructions for four int8 codes, two for four of e4m3).
+// That is 5 to 8 % more than in 16 bits on the same card: the conversions and addresses are vector and scalar work of
 // the same waves (without either: 3.5 ms).  Measured on the way, e4m3:
 //   codes fetched and widened at the end of two tiles, by flat loads          4.74 ms
 //   by global loads (every LDS read waits for a flat load)                    4.59 ms

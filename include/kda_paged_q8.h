@@ -16,7 +16,8 @@
  *   KDA_INT8  c is the signed number, -127 .. 127
  *
  * Scales are powers of two, 2^-126 at least: a division by one is exact, so that the code is the only
- * rounding, and every value of the cache (4 or 7 significant bits) is a bf16 number.  All three
+ * rounding, and every value of the cache (4 or 7 significant bits) is a bf16 number (but for e4m3's below
+ * 2^-133, at scales below 2^-124).  All three
  * read a scale by its exponent: one that is no power of two (from elsewhere, as the largest magnitude
  * over 448) counts as the next power of two below, and an append that adds rows to its block
  * leaves a power of two there.
@@ -121,9 +122,9 @@ kda_status kda_kv_read_q8(const kda_kv_read_q8_args *a);
  *
  * The values' magnitudes stay below 2^99 (rows in fp16: 65520).  In fp16 the values are rounded to
  * fp16 first, which changes only those below its normal numbers.  Scores, sums and softmax statistics
- * are fp32.  Probabilities are rounded to q's type, or, where a request has up to 32 rows per kv head,
- * to bf16 after the product with V's scale: as a pair of bf16 (16 bits) up to 16 rows and in
- * fp16.  What a hidden position's codes and its
+ * are fp32.  Probabilities are rounded to q's type, or, in a call whose requests have up to 32 rows per kv
+ * head (by max_new_len), to bf16 after the product with V's scale: as a pair of bf16 (16 bits) up to 16
+ * rows and in fp16.  What a hidden position's codes and its
  * block's scale hold does not reach a row that does not see it.
  *
  * Errors: as kda_paged_attention, and KDA_ERR_DTYPE for fp32 or an unknown code.
